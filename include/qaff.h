@@ -374,6 +374,113 @@ qaff_status qaff_dequant_rows(const uint32_t* packed, const uint16_t* scales, co
                               const uint32_t* indices, int64_t n_indices,
                               void* out, qaff_dtype out_dtype, hipStream_t stream);
 
+/*
+ * Serving a step around a paged cache. A cache holds the keys (or values) of every request in pages
+ * of page_size tokens: [pages, kv_heads, page_size, head_dim], each page contiguous, page_stride
+ * elements apart (so one allocation may interleave K and V pages). A slot, page * page_size + offset,
+ * names one token's place; a request's block table lists its pages in the order of its tokens.
+ * page_size is 8, 16, 32, 64, 128 or 256 (else QAFF_ERR_UNSUPPORTED). Types are bf16 or float16,
+ * one for q, k, v, the caches and the output. The three entry points below make one layer's step:
+ * the plan (once a step), then per layer the rotary positions with the write into the cache, then
+ * attention of the new tokens over it.
+ *
+ * qaff_paged_plan: block tables and slots of the step's new tokens, from the request lengths alone
+ * (all on the device: nothing is read back).
+ *   cached_lens, new_lens int32 [requests]: tokens in the cache and tokens of this step (negative
+ *   counts as 0); free_pages int32 [n_free]: pages that no request holds, taken in order;
+ *   block_tables int32 [requests, table_width]: entry i of request b is its i-th page; entries
+ *   below ceil(cached / page_size) are read, the entries of the pages this step adds are written.
+ *   Pages go to requests in order, each taking ceil((cached + new) / page_size) -
+ *   ceil(cached / page_size) of them (none if new is 0). Outputs:
+ *   cu_new int32 [requests + 1]: exclusive prefix sums of new_lens;
+ *   kv_lens int32 [requests]: cached + new;
+ *   positions int32 [tokens], slots int64 [tokens]: of new token t of request b (cu_new[b] <= t <
+ *   cu_new[b + 1]), cached[b] + t - cu_new[b] and its slot;
+ *   pages_used int32 [1]: free pages the step takes.
+ *   tokens is the rows of positions and slots: rows past the step's tokens get position 0 and slot
+ *   -1, and tokens past the rows get neither a row nor their pages. Where the free pages or the
+ *   table's width run out, the entry is -1 (where the table has it) and so are the slots of its
+ *   tokens; pages_used then says more than n_free. Sums past 2^31 - 1 saturate.
+ * Errors: INVALID_ARGUMENT for negative sizes, null or misaligned pointers; UNSUPPORTED for a page
+ * size not listed above, more than 16384 requests, or 2^31 tokens or more.
+ */
+qaff_status qaff_paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int64_t requests,
+                            const int32_t* free_pages, int64_t n_free, int32_t* block_tables,
+                            int64_t table_width, int32_t page_size, int64_t tokens, int32_t* cu_new,
+                            int32_t* kv_lens, int32_t* positions, int64_t* slots, int32_t* pages_used,
+                            hipStream_t stream);
+
+/*
+ * Rotary positions of the step's q and k, with the write of k and v into the paged caches.
+ *   q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim] of dtype, with token and head
+ *   strides in elements (the last axis contiguous): views of one projection's rows will do;
+ *   positions int32 [axes, tokens]; inv_freq float32 [rot / 2]; the first rot values of a head turn
+ *   in pairs, pair i by the angle positions[axis(i), t] * inv_freq[i] (the product and its reduction
+ *   to a turn in float64, so far positions keep their angle; sine and cosine in float32):
+ *   (x, y) -> (x cos - y sin, y cos + x sin), x and y being values i and i + rot / 2 of the head, or
+ *   2 i and 2 i + 1 where traditional is non-zero; the other values pass.
+ *   axes 1 to 4; sections: a HOST array of axes pair counts that add up to rot / 2 (null for one
+ *   axis). Pair i's axis is the section that holds i, in order; where interleaved is non-zero it is
+ *   i % axes if i / axes < sections[i % axes], and 0 otherwise.
+ *   slots int64 [tokens]: k (turned) and v of token t go to slot slots[t] of the caches; a slot below
+ *   0 or past the caches writes nothing; two tokens of one slot leave either's values.
+ *   q_out [tokens, heads, head_dim] contiguous (may be q itself where q is contiguous).
+ * Float32 arithmetic, rounded to nearest even once at the end.
+ * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, odd rot, rot above head_dim, axes
+ * outside 1 to 4, sections that do not fit, negative strides, null or misaligned pointers;
+ * UNSUPPORTED for a page size not listed above, head_dim above 512, or 2^31 tokens or more.
+ */
+qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_dtype dtype, int64_t tokens,
+                             int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t q_token_stride,
+                             int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, const int32_t* positions,
+                             int32_t axes, const int32_t* sections, int32_t interleaved, int32_t traditional,
+                             const float* inv_freq, int64_t rot, const int64_t* slots, void* k_cache,
+                             void* v_cache, int64_t pages, int64_t page_stride, int32_t page_size, void* q_out,
+                             hipStream_t stream);
+
+/*
+ * Attention of each request's new tokens over its paged cache (which already holds their own keys
+ * and values): out[t, h] = sum_j p_j V[j], p = softmax_j(scale q[t, h] . K[j]) over the keys j that
+ * t sees, with the keys and values of cache head h / (heads / kv_heads).
+ *   Request b's new tokens are rows cu_new[b] .. cu_new[b + 1] - 1, the last of them at position
+ *   kv_lens[b] - 1. A token at position p sees the keys j < kv_lens[b], of these with causal j <= p,
+ *   and with window > 0 j > p - window. A token that sees no key gets zeros (and lse -infinity); so
+ *   does a row past cu_new[requests]. Values and keys that a token does not see do not enter its row,
+ *   whatever they hold.
+ *   q [tokens, heads, head_dim] with token and head strides in elements (the last axis contiguous);
+ *   block_tables int32 [requests, table_width]; cu_new int32 [requests + 1]; kv_lens int32
+ *   [requests]; out [tokens, heads, head_dim] contiguous; lse float32 [tokens, heads] or null: the
+ *   natural logarithm of the sum of exponentials of the scaled scores.
+ *   max_new: the largest number of new tokens of any request, or any bound of it: a hint for the
+ *   choice of kernel. scale > 0.
+ *   A page outside the pool, or past the table, that a request's keys need is never read: rows that
+ *   meet it come out as NaN.
+ *   workspace: a device buffer of at least qaff_paged_attention_workspace_size(...) bytes, 16-byte
+ *   aligned, which the call overwrites (float32 partial sums where the keys of a row are split over
+ *   workgroups, joined in a fixed order); may be NULL where that size is 0. Results are
+ *   deterministic for the same call.
+ * Scores, sums and the softmax's maximum and sum are float32; the probabilities are rounded to dtype
+ * for their product with V, whose sums are float32; out is rounded once at the end.
+ * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, heads not a multiple of kv_heads, a
+ * scale that is not positive and finite, null or misaligned pointers, a short workspace; UNSUPPORTED
+ * for a page size not listed above, head_dim above 256, more than 65536 requests, tokens * heads of
+ * 2^31 or more, or a table of 2^31 tokens or more a request.
+ */
+qaff_status qaff_paged_attention(const void* q, qaff_dtype dtype, int64_t tokens, int64_t heads,
+                                 int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                                 const void* v_cache, int64_t pages, int64_t page_stride, int64_t kv_heads,
+                                 int64_t head_dim, int32_t page_size, const int32_t* block_tables,
+                                 int64_t table_width, const int32_t* cu_new, const int32_t* kv_lens,
+                                 int64_t requests, int64_t max_new, float scale, int32_t causal, int64_t window,
+                                 void* workspace, size_t workspace_bytes, void* out, float* lse,
+                                 hipStream_t stream);
+
+/* Bytes of workspace qaff_paged_attention needs for these sizes (0: none). */
+size_t qaff_paged_attention_workspace_size(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                           int32_t page_size, int64_t table_width, int64_t requests,
+                                           int64_t max_new);
+
 /* Text for the last non-OK status returned on the calling thread ("" if none). The pointer stays
  * valid until the thread's next qaff call. */
 const char* qaff_last_error(void);

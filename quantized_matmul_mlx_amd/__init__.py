@@ -17,6 +17,12 @@ bit views are accepted too). A weight is ``scale * code + bias`` of its group.
     y = gemv_silu_gate(g, u, packed, scales, biases, group_size, bits, resid=r)  # W . (silu(g) * u) + r
     y = gather_qmm(x, packed, scales, biases, group_size, bits, rhs_indices=experts,
                    sorted_indices=True)                     # batch i: x[i] . dequantize(W[experts[i]])^T
+
+Between the projections of a decoder layer, a serving step over a paged cache (``paged``):
+
+    plan = paged_plan(cached_lens, new_lens, free_pages, block_tables, page_size, tokens)
+    q = rope_append(q, k, v, plan.positions, inv_freq, plan.slots, k_cache, v_cache)
+    o = paged_attention(q, k_cache, v_cache, block_tables, plan.cu_new, plan.kv_lens)
 """
 from __future__ import annotations
 
@@ -27,9 +33,10 @@ import torch
 
 from . import _lib
 from ._lib import QaffError
+from .paged import PagedPlan, paged_attention, paged_plan, rope_append
 
 __all__ = ["quantize", "dequantize", "qmm", "qmm_nt", "dequant_rows", "gemv_gate_up", "gemv_silu_gate", "gather_qmm", "QWeight",
-           "QaffError", "gemv_max_m", "gemv_mfma_min_m"]
+           "QaffError", "gemv_max_m", "gemv_mfma_min_m", "PagedPlan", "paged_plan", "rope_append", "paged_attention"]
 
 _PACKED_DTYPES = (torch.int32, torch.uint32)
 _BF16_BITS_DTYPES = (torch.bfloat16, torch.int16, torch.uint16)

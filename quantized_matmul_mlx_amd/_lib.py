@@ -26,7 +26,8 @@ EXPORTS = ("qaff_dequantize", "qaff_qmm", "qaff_qmm_ex", "qaff_dequant_rows", "q
            "qaff_qmm_nt_static_max_bytes", "qaff_qmm_ws", "qaff_qmm_workspace_size",
            "qaff_promote_dtype",
            "qaff_dequantize_typed", "qaff_qmm_typed", "qaff_quantize_typed", "qaff_gather_qmm_typed",
-           "qaff_qmm_nt_typed")
+           "qaff_qmm_nt_typed", "qaff_paged_plan", "qaff_rope_append", "qaff_paged_attention",
+           "qaff_paged_attention_workspace_size")
 
 ABI_VERSION = 1
 
@@ -79,7 +80,15 @@ def load() -> ctypes.CDLL:
     lib.qaff_gather_qmm_ex.argtypes = gather + [ctypes.c_int]
     lib.qaff_gather_qmm_typed.argtypes = [vp, ctypes.c_int, i64, i64, vp, vp, vp, ctypes.c_int, i64, i64, i64, i32,
                                           i32, vp, vp, i64, i32, vp, vp]
-    for f in (lib.qaff_dequantize, lib.qaff_qmm, lib.qaff_qmm_ex, lib.qaff_dequant_rows,
+    size, f32 = ctypes.c_size_t, ctypes.c_float
+    lib.qaff_paged_plan.argtypes = [vp, vp, i64, vp, i64, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp]
+    lib.qaff_rope_append.argtypes = [vp, vp, vp, ctypes.c_int, *[i64] * 10, vp, i32, vp, i32, i32, vp, i64, vp, vp, vp,
+                                     i64, i64, i32, vp, vp]
+    lib.qaff_paged_attention.argtypes = [vp, ctypes.c_int, i64, i64, i64, i64, vp, vp, i64, i64, i64, i64, i32, vp,
+                                         i64, vp, vp, i64, i64, f32, i32, i64, vp, size, vp, vp, vp]
+    lib.qaff_paged_attention_workspace_size.argtypes = [i64, i64, i64, i64, i32, i64, i64, i64]
+    lib.qaff_paged_attention_workspace_size.restype = size
+    for f in (lib.qaff_paged_plan, lib.qaff_rope_append, lib.qaff_paged_attention, lib.qaff_dequantize, lib.qaff_qmm, lib.qaff_qmm_ex, lib.qaff_dequant_rows,
               lib.qaff_gemv_gate_up, lib.qaff_gemv_silu_gate, lib.qaff_gather_qmm, lib.qaff_gather_qmm_ex,
               lib.qaff_gather_qmm_typed,
               lib.qaff_quantize, lib.qaff_quantize_typed, lib.qaff_qmm_nt, lib.qaff_qmm_nt_static,

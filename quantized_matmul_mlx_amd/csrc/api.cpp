@@ -127,6 +127,14 @@ qaff_status dequant_common(const char* op, const uint32_t* packed, const uint16_
 
 namespace qaff {
 
+void set_error(const char* text) noexcept {
+    try {
+        g_error = text;
+    } catch (...) {
+        g_error.clear();
+    }
+}
+
 int device_cu_count() {
     static std::mutex mu;
     static std::vector<int> cache;

@@ -1,0 +1,114 @@
+// qaff_paged_plan: block tables and slots of a step's new tokens from the request lengths.
+//
+// Request b's tokens start at cu_b = sum of new before b, its new pages at f_b = sum of new pages
+// before b in the free list. The work is a few bytes a token; a launch bounds it. So there is one
+// launch: every workgroup scans all requests itself (two int32 arrays in LDS, 8 bytes a request)
+// instead of waiting for another kernel's scan, then each thread finds one token's request by a
+// binary search in LDS.
+#include "paged.h"
+
+namespace qaff {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWaves = kPlanThreads / 64;
+
+__device__ __forceinline__ int32_t saturated(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : (int32_t)v; }
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
+    extern __shared__ int32_t lds[];
+    __shared__ int64_t wave_sum[2][kPlanWaves];
+    int32_t* cu = lds;                        // [requests + 1]
+    int32_t* page0 = lds + a.requests + 1;    // [requests + 1]
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int64_t round = (1 << a.page_shift) - 1;
+    const bool first = blockIdx.x == 0;
+    int64_t n_before = 0, p_before = 0;
+    for (int b0 = 0; b0 < a.requests; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int64_t n = 0, p = 0;
+        if (b < a.requests) {
+            const int64_t c = max(a.cached[b], 0);
+            n = max(a.fresh[b], 0);
+            if (n > 0) p = ((c + n + round) >> a.page_shift) - ((c + round) >> a.page_shift);
+            if (first) a.kv_lens[b] = saturated(c + n);
+        }
+        const int64_t n_in = wave_scan(n), p_in = wave_scan(p);
+        if ((tid & 63) == 63) {
+            wave_sum[0][wave] = n_in;
+            wave_sum[1][wave] = p_in;
+        }
+        __syncthreads();
+        int64_t n_all = n_before, p_all = p_before, n_at = n_before, p_at = p_before;
+        for (int w = 0; w < kPlanWaves; ++w) {
+            if (w == wave) n_at = n_all, p_at = p_all;
+            n_all += wave_sum[0][w];
+            p_all += wave_sum[1][w];
+        }
+        if (b < a.requests) {
+            cu[b] = saturated(n_at + n_in - n);
+            page0[b] = saturated(p_at + p_in - p);
+        }
+        n_before = n_all;
+        p_before = p_all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        cu[a.requests] = saturated(n_before);
+        if (first) a.pages_used[0] = saturated(p_before);
+    }
+    __syncthreads();
+    if (first)
+        for (int b = tid; b <= a.requests; b += kPlanThreads) a.cu_new[b] = cu[b];
+
+    const int64_t t = (int64_t)blockIdx.x * kPlanThreads + tid;
+    if (t >= a.tokens) return;
+    int32_t pos = 0;
+    int64_t slot = -1;
+    if (t < cu[a.requests]) {
+        int lo = 0, hi = a.requests;  // cu[lo] <= t < cu[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        const int64_t c = max(a.cached[lo], 0);
+        const int64_t p = c + (t - cu[lo]);
+        const int64_t have = (c + round) >> a.page_shift, at = p >> a.page_shift;
+        int32_t* entry = a.tables + (int64_t)lo * a.table_width + at;
+        int32_t page = -1;
+        if (at < have) {
+            if (at < a.table_width) page = *entry;
+        } else {
+            const int64_t f = page0[lo] + (at - have);
+            if (f < a.n_free && at < a.table_width) page = a.free_pages[f];
+            // a new page's first token is a new token (have is rounded up), so it writes the entry
+            if ((p & round) == 0 && at < a.table_width) *entry = page;
+        }
+        pos = saturated(p);
+        if (page >= 0) slot = ((int64_t)page << a.page_shift) + (p & round);
+    }
+    a.positions[t] = pos;
+    a.slots[t] = slot;
+}
+
+}  // namespace
+
+hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(a.tokens > 0 ? (a.tokens + kPlanThreads - 1) / kPlanThreads : 1);
+    paged_plan_kernel<<<grid, kPlanThreads, (size_t)(a.requests + 1) * 8, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace qaff
