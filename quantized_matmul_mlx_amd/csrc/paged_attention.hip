@@ -96,15 +96,567 @@ __global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
     if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads + h] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// ---- The matrix-core kernel ----
+//
+// A request's query heads that share a cache head are rows of one matrix: row r of the request is its
+// token r / group with head r % group of the group, so every tile of keys is read once for all of
+// them. A wave holds 32 rows and takes keys 32 at a time with v_mfma_f32_32x32x16:
+//   S^T = K . Q^T   (A = 32 keys x 16 values from LDS, B = Q^T in registers)
+//   O^T += V^T . P^T (A = V^T by transposing LDS reads, B = P^T)
+// Transposed, a lane holds 16 scores of ONE row (lane % 32): its softmax needs one exchange between
+// the wave's halves, and its rescaling factor is the lane's own. The lane's scores also are what B
+// wants of P^T, if the 16 keys of a product are numbered as they lie: half h holds keys 4 h .. 4 h + 3
+// and 8 + 4 h .. 8 + 4 h + 3 of each 16, and the reads of V^T take the same order.
+//
+// NW waves make a workgroup of 32 NW rows: NW = 4 for chunks and prompts (keys staged once for 128
+// rows), NW = 1 where a request has at most 32 rows (decode), there with the keys of a request split
+// over as many workgroups as fill the chip.
+//
+// K and V tiles go through registers into LDS one tile ahead. LDS holds 16-byte pieces, piece c of
+// row r at c ^ f(r), so that neither the row-wise reads of K nor the transposing reads of V (4 rows
+// by 64 bytes for half a wave) meet in a bank.
+
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+struct Sched {
+    int rows_lo, rows_hi;  // takes requests with rows_lo < rows <= rows_hi (rows = tokens * group)
+    int parts;             // tiles of rows are cut along the keys into about so many parts in all; 0: not cut
+    float* part_o;         // [item, kv head, row of the tile, dim] sums of a part
+    float2* part_ml;       // their running maximum (log2) and sum
+};
+
+// A workgroup's work: part `part` of `parts` of a tile of a request's rows.
+struct Item {
+    int tile, part, parts;
+    int first;       // the item of part 0
+    int row_end;     // rows of the request
+    int start, end;  // its rows of q, as cu gives them
+    int kv;
+    int b;
+};
+
+constexpr int kMinPart = 2;  // key tiles a part has at least
+
+// Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
+// Every wave scans the requests itself, 64 at a time: with up to 63 requests that is one load of
+// each length and a few cross-lane sums, less than reading another kernel's schedule would cost.
+// Rows past the last request are one more request without keys.
+template <int ROWS, int KT>
+__device__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_tile, Item& it) {
+    const int lane = threadIdx.x & 63;
+    const int count = a.requests + 1;
+    const int per_tile = ROWS / a.group + 2;  // tokens a tile may touch
+    int start = 0, end = 0, kv = 0, tiles = 0, span = 0;
+    auto load = [&](int b) {
+        start = end = kv = tiles = span = 0;
+        if (b < a.requests) {
+            start = a.cu[b];
+            end = a.cu[b + 1];
+            kv = max(a.kv_lens[b], 0);
+        } else if (b == a.requests) {
+            start = a.cu[b];
+            end = a.tokens;
+        }
+        if (start >= 0 && end > start && end <= a.tokens) {
+            const int64_t rows = (int64_t)(end - start) * a.group;
+            if (rows > s.rows_lo && rows <= s.rows_hi) tiles = (int)((rows + ROWS - 1) / ROWS);
+        }
+        int64_t keys = kv;
+        if (a.window > 0) keys = min(keys, a.window + per_tile + KT);
+        span = (int)((keys + KT - 1) / KT);
+    };
+    load(lane);
+    int64_t len = 1LL << 40;  // key tiles a part has
+    if (s.parts > 0) {
+        int64_t total = (int64_t)tiles * span;
+        for (int b0 = 64; b0 < count; b0 += 64) {
+            load(b0 + lane);
+            total += (int64_t)tiles * span;
+        }
+        for (int x = 32; x > 0; x >>= 1) total += __shfl_xor(total, x);
+        len = max((int64_t)kMinPart, (total + s.parts - 1) / s.parts);
+        if (count > 64) load(lane);
+    }
+    int items_before = 0, tiles_before = 0;
+    for (int b0 = 0;; b0 += 64) {
+        const int parts = max(1, (int)((span + len - 1) / len));
+        const int items = tiles * parts;
+        int items_in = items, tiles_in = tiles;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(items_in, d), w = __shfl_up(tiles_in, d);
+            if (lane >= d) items_in += u, tiles_in += w;
+        }
+        const int upto = by_tile ? tiles_before + tiles_in : items_before + items_in;
+        const uint64_t past = __ballot(upto > want);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            const int base = __shfl(items_before + items_in - items, at);
+            const int n = __shfl(parts, at), t = __shfl(tiles, at);
+            const int local = by_tile ? want - __shfl(tiles_before + tiles_in - tiles, at) : (want - base) / n;
+            it.first = base + local * n;
+            it.part = by_tile ? 0 : want - it.first;
+            it.parts = n;
+            it.tile = t - 1 - local;  // a causal prompt's last rows see the most keys: they go first
+            it.start = __shfl(start, at);
+            it.end = __shfl(end, at);
+            it.kv = __shfl(kv, at);
+            it.row_end = (it.end - it.start) * a.group;
+            it.b = b0 + at;
+            return true;
+        }
+        items_before += __shfl(items_in, 63);
+        tiles_before += __shfl(tiles_in, 63);
+        if (b0 + 64 >= count) return false;
+        load(b0 + 64 + lane);
+    }
+}
+
+// The keys [lo, hi) that token i of the request sees.
+__device__ __forceinline__ void seen_keys(const AttnArgs& a, const Item& it, int i, int& lo, int& hi) {
+    const int pos = it.kv - (it.end - it.start) + i;
+    hi = a.causal ? max(0, min(it.kv, pos + 1)) : it.kv;
+    lo = a.window > 0 ? (int)max((int64_t)0, pos + 1 - a.window) : 0;
+}
+
+// The other half-wave's value joined with this one's.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Whether either 16-bit value of w is infinite or NaN.
+template <bool F16>
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+    constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
+    return (w & E) == E || ((w >> 16) & E) == E;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
+    constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
+    return ((w & E) == E ? 0u : w & 0xFFFFu) | (((w >> 16) & E) == E ? 0u : w & 0xFFFF0000u);
+}
+
+template <int DP> __device__ __forceinline__ int swizzle_k(int row) { return DP == 64 ? (row >> 1) & 7 : row & 15; }
+template <int DP> __device__ __forceinline__ int swizzle_v(int row) { return DP == 64 ? (row & 2) << 1 : (row & 3) << 2; }
+
+// float16 probabilities carry a factor 2^7 (which the division by their sum takes out again): their
+// smallest step is then 2^-31 of the largest, so long rows of small weights are not lost. With the
+// slack of the running maximum below they stay under 2^15.
+template <bool F16> constexpr float kLift = F16 ? 7.f : 0.f;
+// The running maximum follows a row's true one only once that is 2^8 times larger: a stale maximum
+// scales sums and probabilities alike, and most tiles then need no rescaling of the output sums.
+constexpr float kSlack = 8.f;
+
+template <bool F16, int DP, int NW, int KT>
+__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArgs a, Sched s) {
+    constexpr int ROWS = 32 * NW, NT = 64 * NW;
+    constexpr int CH = DP / 8;               // 16-byte pieces of a row
+    constexpr int PER = KT * CH / NT;        // pieces of a tile per thread, RSTEP rows apart
+    constexpr int RSTEP = NT / CH;
+    constexpr int KB = KT / 32;
+    constexpr int BUF = NW > 1 ? 2 : 1;
+    constexpr int TILE = KT * DP;            // elements
+    __shared__ __align__(16) uint16_t lds[BUF][2][TILE];
+
+    const int hk = blockIdx.x % a.kv_heads;
+    const int item = blockIdx.x / a.kv_heads;
+    Item it;
+    if (!find_item<ROWS, KT>(a, s, item, false, it)) return;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int half = lane >> 5, col = lane & 31;
+    const int r0 = it.tile * ROWS;
+    const int rows = min(ROWS, it.row_end - r0);
+    // this lane's row
+    const int r = wave * 32 + col;
+    const bool live = r < rows;
+    const int token = (r0 + min(r, rows - 1)) / a.group;
+    const int head = hk * a.group + (r0 + min(r, rows - 1)) - token * a.group;
+    int lo, hi;
+    seen_keys(a, it, token, lo, hi);
+    // keys the workgroup reads: from the first that its first token sees to the last of its last
+    int lo_all, hi_all, unused;
+    seen_keys(a, it, r0 / a.group, lo_all, unused);
+    seen_keys(a, it, (r0 + rows - 1) / a.group, unused, hi_all);
+    const int kt0 = lo_all / KT;
+    const int n_all = max(0, (hi_all + KT - 1) / KT - kt0);
+    const int kt_begin = kt0 + (int)((int64_t)n_all * it.part / it.parts);
+    const int kt_end = kt0 + (int)((int64_t)n_all * (it.part + 1) / it.parts);
+    // the wave's tiles below sure_hi and from sure_lo on need no mask; rows that are not there
+    // need none either
+    int sure_lo = live ? lo : 0, sure_hi = live ? hi : 0x7fffffff, any_hi = live ? hi : 0;
+    for (int x = 16; x > 0; x >>= 1) {
+        sure_lo = max(sure_lo, __shfl_xor(sure_lo, x));
+        sure_hi = min(sure_hi, __shfl_xor(sure_hi, x));
+        any_hi = max(any_hi, __shfl_xor(any_hi, x));
+    }
+
+    // Q^T in registers: lane holds row `col`, values 16 c + 8 half ..
+    op8<F16> q[DP / 16];
+    {
+        const uint16_t* src = a.q + (int64_t)(it.start + token) * a.q_ts + (int64_t)head * a.q_hs;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const int d = 16 * c + 8 * half;
+            u32x4a v = {0, 0, 0, 0};
+            if (live && d < a.dim) v = *reinterpret_cast<const u32x4a*>(src + d);
+            q[c] = __builtin_bit_cast(op8<F16>, v);
+        }
+    }
+
+    // staging: this thread's pieces are rows row0 + RSTEP i, piece `piece`
+    const int row0 = tid / CH, piece = tid % CH;
+    const bool piece_in = piece * 8 < a.dim;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
+    const uint16_t* kc = a.k_cache + ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
+    const uint16_t* vc = a.v_cache + ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
+    int page[PER];
+    u32x4a kreg[PER], vreg[PER];
+    auto load_pages = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int key = kt * KT + row0 + RSTEP * i;
+            page[i] = -1;
+            if (key < hi_all && (key >> a.page_shift) < a.table_width) page[i] = table[key >> a.page_shift];
+        }
+    };
+    auto load_tile = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int key = kt * KT + row0 + RSTEP * i;
+            u32x4a kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
+            if (key >= lo_all && key < hi_all) {
+                if ((uint32_t)page[i] < (uint64_t)a.pages) {
+                    if (piece_in) {
+                        const int64_t at = page[i] * a.page_stride + (int64_t)(key & page_mask) * a.dim;
+                        kv = *reinterpret_cast<const u32x4a*>(kc + at);
+                        vv = *reinterpret_cast<const u32x4a*>(vc + at);
+                    }
+                } else {  // outside the pool: NaN scores, so the rows that see the key are NaN
+                    kv = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
+                }
+            }
+            kreg[i] = kv;
+            vreg[i] = vv;
+        }
+    };
+
+    f32x16 acc[DP / 32];
+#pragma unroll
+    for (int n = 0; n < DP / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[n][i] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const float factor = a.scale * kLog2e;
+
+    // addresses of a lane's reads, in elements
+    const int v_row = 4 * half + ((lane & 15) >> 2);                          // + 16 c + 8 e + 32 kb
+    const int v_piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);            // + 4 n
+    const int v_sub = 4 * (lane & 1);
+
+    if (kt_begin < kt_end) {
+        load_pages(kt_begin);
+        load_tile(kt_begin);
+        load_pages(kt_begin + 1);
+    }
+    for (int kt = kt_begin; kt < kt_end; ++kt) {
+        uint16_t* kl = lds[BUF > 1 ? kt & 1 : 0][0];
+        uint16_t* vl = lds[BUF > 1 ? kt & 1 : 0][1];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int row = row0 + RSTEP * i;
+            *reinterpret_cast<u32x4a*>(kl + row * DP + ((piece ^ swizzle_k<DP>(row)) * 8)) = kreg[i];
+            *reinterpret_cast<u32x4a*>(vl + row * DP + ((piece ^ swizzle_v<DP>(row)) * 8)) = vreg[i];
+        }
+        if (kt + 1 < kt_end) {
+            load_tile(kt + 1);
+            load_pages(kt + 2);
+        }
+        // two buffers: the other one's readers are past the previous barrier
+        if (NW > 1) __syncthreads();
+        const int key0 = kt * KT;
+        if (key0 >= any_hi) continue;  // keys past every row of this wave
+
+        f32x16 sc[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int row = kb * 32 + col;
+                const op8<F16> kf = *reinterpret_cast<const op8<F16>*>(
+                    kl + row * DP + (((2 * c + half) ^ swizzle_k<DP>(row)) * 8));
+                sc[kb] = mfma32x32x16<F16>(kf, q[c], sc[kb]);
+            }
+        }
+        const bool masked = key0 < sure_lo || key0 + KT > sure_hi;
+        if (masked) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = key0 + kb * 32 + (i >> 2) * 8 + 4 * half + (i & 3);
+                    if (key < lo || key >= hi) sc[kb][i] = -INFINITY;
+                }
+        }
+        float top = sc[0][0];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
+        top = max_halves(top) * factor;
+        if (__any(top > m + kSlack)) {
+            const float m_new = fmaxf(m, top);
+            const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+            l *= keep;
+#pragma unroll
+            for (int n = 0; n < DP / 32; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[n][i] *= keep;
+            m = m_new;
+        }
+        const float base = m == -INFINITY ? 0.f : m - kLift<F16>;
+        op8<F16> p[KB][2];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sc[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[kb][i], factor, -base));
+                l += sc[kb][i];
+            }
+            // rounded to 16 bits for the product with V; their sum l is taken before the rounding
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                p[kb][c] = __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(sc[kb][8 * c], sc[kb][8 * c + 1]),
+                                                               pack_half2<F16>(sc[kb][8 * c + 2], sc[kb][8 * c + 3]),
+                                                               pack_half2<F16>(sc[kb][8 * c + 4], sc[kb][8 * c + 5]),
+                                                               pack_half2<F16>(sc[kb][8 * c + 6], sc[kb][8 * c + 7])});
+        }
+        // A weight of zero times an infinite or NaN value is NaN: where the tile holds keys that some
+        // row does not see, look for such values, and keep them out of the products.
+        bool careful = false;
+        if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) {
+            for (int x = lane; x < TILE / 8; x += 64) {
+                const u32x4a w = *reinterpret_cast<const u32x4a*>(vl + x * 8);
+                careful |= not_finite2<F16>(w.x) || not_finite2<F16>(w.y) || not_finite2<F16>(w.z) ||
+                           not_finite2<F16>(w.w);
+            }
+            careful = __any(careful);
+        }
+#pragma unroll
+        for (int n = 0; n < DP / 32; ++n) {
+            const int at = ((v_piece + 4 * n) ^ swizzle_v<DP>(v_row)) * 8 + v_sub;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint16_t* src = vl + (v_row + 32 * kb + 16 * c) * DP + at;
+                    const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
+                    const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 8 * DP));
+                    const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
+                    u32x4a w = {w0.x, w0.y, w1.x, w1.y};
+                    if (careful)
+                        w = u32x4a{finite_or_zero2<F16>(w.x), finite_or_zero2<F16>(w.y), finite_or_zero2<F16>(w.z),
+                                   finite_or_zero2<F16>(w.w)};
+                    acc[n] = mfma32x32x16<F16>(__builtin_bit_cast(op8<F16>, w), p[kb][c], acc[n]);
+                }
+        }
+        if (careful) {  // what was kept out goes to the rows that see it, one key at a time
+            for (int j = 0; j < KT; ++j) {
+                const bool sees = key0 + j >= lo && key0 + j < hi;
+#pragma unroll
+                for (int n = 0; n < DP / 32; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int d = 32 * n + (i >> 2) * 8 + 4 * half + (i & 3);
+                        const uint32_t w = vl[j * DP + (((d >> 3) ^ swizzle_v<DP>(j)) * 8) + (d & 7)];
+                        if (sees && not_finite2<F16>(w)) acc[n][i] += half_to_f32<F16>(w);
+                    }
+            }
+        }
+    }
+
+    l = add_halves(l);
+    if (!live) return;
+    const float m_out = m - kLift<F16>;
+    if (it.parts > 1) {
+        const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + r;
+        float* o = s.part_o + slot * a.dim;
+#pragma unroll
+        for (int n = 0; n < DP / 32; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = 32 * n + 8 * i + 4 * half;
+                if (d < a.dim)
+                    *reinterpret_cast<f32x4*>(o + d) =
+                        f32x4{acc[n][4 * i], acc[n][4 * i + 1], acc[n][4 * i + 2], acc[n][4 * i + 3]};
+            }
+        if (half == 0) s.part_ml[slot] = make_float2(m_out, l);
+        return;
+    }
+    const bool empty = hi <= lo;
+    const float inv = empty ? 0.f : 1.f / l;
+    const int64_t row = (int64_t)(it.start + token) * a.heads + head;
+    uint16_t* o = a.out + row * a.dim;
+#pragma unroll
+    for (int n = 0; n < DP / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = 32 * n + 8 * i + 4 * half;
+            if (d < a.dim)
+                *reinterpret_cast<uint2*>(o + d) = make_uint2(pack_half2<F16>(acc[n][4 * i] * inv, acc[n][4 * i + 1] * inv),
+                                                              pack_half2<F16>(acc[n][4 * i + 2] * inv, acc[n][4 * i + 3] * inv));
+        }
+    if (a.lse && half == 0) a.lse[row] = empty ? -INFINITY : (m_out + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// Joins the parts of a tile's rows, in their order: o = sum_s w_s o_s / sum_s w_s l_s with
+// w_s = 2^(m_s - max m). A workgroup takes one row of a tile at a time; DP / 4 threads hold the row
+// and the others take other parts.
+template <bool F16, int DP, int ROWS, int KT>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
+    constexpr int LANES = DP / 4, GROUPS = 256 / LANES;
+    __shared__ f32x4 so[GROUPS][LANES];
+    __shared__ float2 sml[GROUPS];
+    const int hk = blockIdx.x % a.kv_heads;
+    Item it;
+    if (!find_item<ROWS, KT>(a, s, blockIdx.x / a.kv_heads, true, it) || it.parts == 1) return;
+    const int x = threadIdx.x % LANES, g = threadIdx.x / LANES;
+    const int r0 = it.tile * ROWS, rows = min(ROWS, it.row_end - r0);
+    const bool in = 4 * x < a.dim;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        float m = -INFINITY, l = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int p = g; p < it.parts; p += GROUPS) {
+            const int64_t slot = ((int64_t)(it.first + p) * a.kv_heads + hk) * ROWS + r;
+            const float2 ml = s.part_ml[slot];
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (in) v = *reinterpret_cast<const f32x4*>(s.part_o + slot * a.dim + 4 * x);
+            const float m_new = fmaxf(m, ml.x);
+            const float base = m_new == -INFINITY ? 0.f : m_new;
+            const float k0 = __builtin_amdgcn_exp2f(m - base), k1 = __builtin_amdgcn_exp2f(ml.x - base);
+            l = l * k0 + ml.y * k1;
+            o = o * k0 + v * k1;
+            m = m_new;
+        }
+        __syncthreads();
+        so[g][x] = o;
+        if (x == 0) sml[g] = make_float2(m, l);
+        __syncthreads();
+        if (g != 0) continue;
+        for (int p = 1; p < GROUPS; ++p) {
+            const float2 ml = sml[p];
+            const float m_new = fmaxf(m, ml.x);
+            const float base = m_new == -INFINITY ? 0.f : m_new;
+            const float k0 = __builtin_amdgcn_exp2f(m - base), k1 = __builtin_amdgcn_exp2f(ml.x - base);
+            l = l * k0 + ml.y * k1;
+            o = o * k0 + so[p][x] * k1;
+            m = m_new;
+        }
+        const int token = (r0 + r) / a.group, head = hk * a.group + (r0 + r) - token * a.group;
+        int lo, hi;
+        seen_keys(a, it, token, lo, hi);
+        const bool empty = hi <= lo;
+        const float inv = empty ? 0.f : 1.f / l;
+        const int64_t row = (int64_t)(it.start + token) * a.heads + head;
+        if (in)
+            *reinterpret_cast<uint2*>(a.out + row * a.dim + 4 * x) =
+                make_uint2(pack_half2<F16>(o.x * inv, o.y * inv), pack_half2<F16>(o.z * inv, o.w * inv));
+        if (a.lse && x == 0) a.lse[row] = empty ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    }
+}
+
+// How a call runs: the few-rows kernel (32-row tiles), the many-rows kernel (128-row tiles) or both,
+// and whether their tiles are cut along the keys.
+struct Launches {
+    struct One {
+        int64_t tiles = 0;  // at most so many tiles (0: not launched)
+        int rows = 0, rows_lo = 0, rows_hi = 0;
+        int parts = 0;
+        int64_t items() const { return tiles + parts; }
+        size_t slots(int64_t kv_heads) const { return parts ? (size_t)(items() * kv_heads * rows) : 0; }
+    } few, many;
+};
+
+Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
+                       int64_t requests, int64_t max_new) {
+    Launches p;
+    const int64_t group = heads / kv_heads, rows = tokens * group, cus = device_cu_count();
+    const int64_t holders = requests + 1 < tokens ? requests + 1 : tokens;  // requests with rows
+    const bool one = requests == 1 && rows > 32;
+    if (max_new * group <= 32 || rows <= 32) {
+        p.few.tiles = holders + rows / 32;
+        p.few.rows_hi = 0x7fffffff;
+    } else {
+        if (!one) {
+            p.few.tiles = holders;
+            p.few.rows_hi = 32;
+            p.many.rows_lo = 32;
+        }
+        p.many.tiles = rows / 128 + (holders < rows / 33 + 1 ? holders : rows / 33 + 1);
+        p.many.rows_hi = 0x7fffffff;
+    }
+    p.few.rows = 32;
+    p.many.rows = 128;
+    // Cut where whole tiles would leave workgroup slots empty: 8 waves of the few-rows kernel fit a
+    // CU, 2 workgroups of the other. Parts have 4 (2) times the slots, so that uneven ends are short.
+    if (p.few.tiles && table_keys > 32 * kMinPart) p.few.parts = (int)((cus * 16 + kv_heads - 1) / kv_heads);
+    const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
+    if (p.many.tiles && p.many.tiles < slots && table_keys > 64 * kMinPart) p.many.parts = (int)(2 * slots);
+    (void)head_dim;
+    return p;
+}
+
+template <bool F16, int DP>
+hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream) {
+    constexpr int KT = DP > 128 ? 32 : 64;
+    const size_t few_slots = p.few.slots(a.kv_heads), many_slots = p.many.slots(a.kv_heads);
+    float* o = a.partial;
+    float2* ml = reinterpret_cast<float2*>(o + (few_slots + many_slots) * a.dim);
+    const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, o, ml};
+    const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, o + few_slots * a.dim, ml + few_slots};
+    if (p.many.tiles)
+        attn_kernel<F16, DP, 4, KT><<<(unsigned)(p.many.items() * a.kv_heads), 256, 0, stream>>>(a, many);
+    if (p.few.tiles) attn_kernel<F16, DP, 1, 32><<<(unsigned)(p.few.items() * a.kv_heads), 64, 0, stream>>>(a, few);
+    if (p.many.parts)
+        join_kernel<F16, DP, 128, KT><<<dim3((unsigned)(p.many.tiles * a.kv_heads), 64), 256, 0, stream>>>(a, many);
+    if (p.few.parts)
+        join_kernel<F16, DP, 32, 32>
+            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < 32 ? a.group : 32), 256, 0, stream>>>(a, few);
+    return hipGetLastError();
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 }  // namespace
 
-size_t paged_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t paged_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
+                                 int64_t requests, int64_t max_new) {
+    const Launches p = plan_launches(tokens, heads, kv_heads, head_dim, table_keys, requests, max_new);
+    return (p.few.slots(kv_heads) + p.many.slots(kv_heads)) * (size_t)(4 * head_dim + 8);
+}
 
-hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t, hipStream_t stream) {
-    const unsigned grid = (unsigned)a.tokens * (unsigned)a.heads;
-    if (f16) attn_scalar_kernel<true><<<grid, 64, 0, stream>>>(a);
-    else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
-    return hipGetLastError();
+hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, hipStream_t stream) {
+    // 16-byte loads of every row, and heads of whole 16-byte pieces
+    const bool pieces = a.dim % 8 == 0 && a.q_ts % 8 == 0 && a.q_hs % 8 == 0 && a.page_stride % 8 == 0 &&
+                        aligned16(a.q) && aligned16(a.k_cache) && aligned16(a.v_cache) && aligned16(a.out);
+    if (!pieces) {
+        const unsigned grid = (unsigned)a.tokens * (unsigned)a.heads;
+        if (f16) attn_scalar_kernel<true><<<grid, 64, 0, stream>>>(a);
+        else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_width << a.page_shift, a.requests, max_new);
+    if (a.dim <= 64) return f16 ? launch_tiles<true, 64>(a, p, stream) : launch_tiles<false, 64>(a, p, stream);
+    if (a.dim <= 128) return f16 ? launch_tiles<true, 128>(a, p, stream) : launch_tiles<false, 128>(a, p, stream);
+    return f16 ? launch_tiles<true, 256>(a, p, stream) : launch_tiles<false, 256>(a, p, stream);
 }
 
 }  // namespace qaff
