@@ -25,29 +25,20 @@ __device__ __forceinline__ int request_of(const AttnArgs& a, int t) {
     return lo;
 }
 
-// One wave per row (token, head), one key per lane, element loads: any head size and alignment.
+// A wave takes one row (token t, head h) over keys [lo, hi) of request b, one key a lane, element
+// loads: any head size and alignment, and nothing but the keys in the range enters. Leaves the running
+// maximum (log2), the sum and o (lane + 64 i) of the range.
 template <bool F16>
-__global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
-    __shared__ float q[256];
-    __shared__ float prob[64];
-    __shared__ int64_t place[64];
-    const int lane = threadIdx.x;
-    const int t = blockIdx.x / a.heads, h = blockIdx.x - t * a.heads;
+__device__ void scalar_row(const AttnArgs& a, int b, int t, int h, int64_t lo, int64_t hi, float& m, float& l,
+                           float (&acc)[4]) {
+    const int lane = threadIdx.x & 63;
     const int hk = h / a.group;
-    const uint16_t* qr = a.q + t * a.q_ts + h * a.q_hs;
-    for (int d = lane; d < a.dim; d += 64) q[d] = half_to_f32<F16>(qr[d]) * (a.scale * kLog2e);
-    __syncthreads();
-    const int b = a.requests > 0 ? request_of(a, t) : -1;
-    int64_t lo = 0, hi = 0;  // keys that the row sees
-    if (b >= 0) {
-        const int64_t kv = a.kv_lens[b];
-        const int64_t pos = kv - a.cu[b + 1] + t;
-        hi = a.causal ? min(kv, pos + 1) : kv;
-        lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
-    }
+    const uint16_t* q = a.q + t * a.q_ts + h * a.q_hs;
     const int page_mask = (1 << a.page_shift) - 1;
-    float m = -INFINITY, l = 0.f;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    m = -INFINITY;
+    l = 0.f;
+    for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+#pragma unroll 1
     for (int64_t j0 = lo; j0 < hi; j0 += 64) {
         const int64_t j = j0 + lane;
         float s = -INFINITY;
@@ -59,7 +50,8 @@ __global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
             if (page >= 0 && page < a.pages) {
                 at = page * a.page_stride + (((int64_t)hk << a.page_shift) + (j & page_mask)) * a.dim;
                 s = 0.f;
-                for (int d = 0; d < a.dim; ++d) s += q[d] * half_to_f32<F16>(a.k_cache[at + d]);
+                for (int d = 0; d < a.dim; ++d) s += half_to_f32<F16>(q[d]) * half_to_f32<F16>(a.k_cache[at + d]);
+                s *= a.scale * kLog2e;
             }
         }
         float top = s;
@@ -72,28 +64,47 @@ __global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
         for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
         l = l * keep + sum;
         m = m_new;
-        __syncthreads();
-        prob[lane] = p;
-        place[lane] = at;
-        __syncthreads();
+        for (int i = 0; i < 4; ++i) acc[i] *= keep;
         const int n = (int)min((int64_t)64, hi - j0);
-        for (int i = 0; i < 4; ++i) {
-            const int d = lane + 64 * i;
-            if (d >= a.dim) break;
-            float o = acc[i] * keep;
-            for (int c = 0; c < n; ++c)
-                o += place[c] < 0 ? prob[c] : prob[c] * half_to_f32<F16>(a.v_cache[place[c] + d]);
-            acc[i] = o;
+        for (int c = 0; c < n; ++c) {
+            const float w = __shfl(p, c);
+            const int64_t from = __shfl(at, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = lane + 64 * i;
+                if (d < a.dim) acc[i] += from < 0 ? w : w * half_to_f32<F16>(a.v_cache[from + d]);
+            }
         }
     }
-    // a row that sees no key: zeros and -infinity
-    const bool empty = hi <= lo;
-    uint16_t* o = a.out + ((int64_t)t * a.heads + h) * a.dim;
+}
+
+// The result of a row that sees no key is zeros and -infinity.
+template <bool F16>
+__device__ void store_scalar_row(const AttnArgs& a, int t, int h, bool empty, float m, float l, const float (&acc)[4]) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)t * a.heads + h;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int d = lane + 64 * i;
-        if (d < a.dim) o[d] = f32_to_half_bits<F16>(empty ? 0.f : acc[i] / l);
+        if (d < a.dim) a.out[row * a.dim + d] = f32_to_half_bits<F16>(empty ? 0.f : acc[i] / l);
     }
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads + h] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <bool F16>
+__global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
+    const int t = blockIdx.x / a.heads, h = blockIdx.x - t * a.heads;
+    const int b = a.requests > 0 ? request_of(a, t) : -1;
+    int64_t lo = 0, hi = 0;  // keys that the row sees
+    if (b >= 0) {
+        const int64_t kv = a.kv_lens[b];
+        const int64_t pos = kv - a.cu[b + 1] + t;
+        hi = a.causal ? min(kv, pos + 1) : kv;
+        lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
+    }
+    float m, l, acc[4];
+    scalar_row<F16>(a, b, t, h, lo, hi, m, l, acc);
+    store_scalar_row<F16>(a, t, h, hi <= lo, m, l, acc);
 }
 
 // ---- The matrix-core kernel ----
@@ -122,6 +133,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 struct Sched {
     int rows_lo, rows_hi;  // takes requests with rows_lo < rows <= rows_hi (rows = tokens * group)
     int parts;             // tiles of rows are cut along the keys into about so many parts in all; 0: not cut
+    int min_part;          // key tiles that a part has at least
     float* part_o;         // [item, kv head, row of the tile, dim] sums of a part
     float2* part_ml;       // their running maximum (log2) and sum
 };
@@ -136,7 +148,6 @@ struct Item {
     int b;
 };
 
-constexpr int kMinPart = 2;  // key tiles a part has at least
 
 // Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
 // Every wave scans the requests itself, 64 at a time: with up to 63 requests that is one load of
@@ -175,7 +186,7 @@ __device__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_t
             total += (int64_t)tiles * span;
         }
         for (int x = 32; x > 0; x >>= 1) total += __shfl_xor(total, x);
-        len = max((int64_t)kMinPart, (total + s.parts - 1) / s.parts);
+        len = max((int64_t)s.min_part, (total + s.parts - 1) / s.parts);
         if (count > 64) load(lane);
     }
     int items_before = 0, tiles_before = 0;
@@ -219,14 +230,25 @@ __device__ __forceinline__ void seen_keys(const AttnArgs& a, const Item& it, int
     lo = a.window > 0 ? (int)max((int64_t)0, pos + 1 - a.window) : 0;
 }
 
-// The other half-wave's value joined with this one's.
-__device__ __forceinline__ float max_halves(float v) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+// The maximum and the sum of v over the lanes that hold the same row: lane and lane ^ 32, and with 16
+// rows a wave lane ^ 16 and lane ^ 48 too.
+template <int R> __device__ __forceinline__ float max_of_row(float v) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    if (R == 16) {
+        r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return v;
 }
-__device__ __forceinline__ float add_halves(float v) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+template <int R> __device__ __forceinline__ float sum_of_row(float v) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if (R == 16) {
+        r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
 }
 
 // Whether either 16-bit value of w is infinite or NaN.
@@ -235,14 +257,31 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
     constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
     return (w & E) == E || ((w >> 16) & E) == E;
 }
-template <bool F16>
-__device__ __forceinline__ uint32_t finite_or_zero2(uint32_t w) {
-    constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
-    return ((w & E) == E ? 0u : w & 0xFFFFu) | (((w >> 16) & E) == E ? 0u : w & 0xFFFF0000u);
+// Where piece c of row r of a tile lies: c ^ f(r). K is read a row a lane (16 lanes: 16 rows, one
+// piece), V in half-waves of 4 rows by 4 pieces (R = 32) or 8 rows by 2 pieces (R = 16): each time the
+// 256 bytes fall into all 64 banks.
+template <int DP> __device__ __forceinline__ int swizzle_k(int row) { return DP == 64 ? (row >> 1) & 7 : row & 15; }
+template <int DP, int R> __device__ __forceinline__ int swizzle_v(int row) {
+    if (R == 16) return DP == 64 ? row & 6 : (row & 7) << 1;
+    return DP == 64 ? (row & 2) << 1 : (row & 3) << 2;
 }
 
-template <int DP> __device__ __forceinline__ int swizzle_k(int row) { return DP == 64 ? (row >> 1) & 7 : row & 15; }
-template <int DP> __device__ __forceinline__ int swizzle_v(int row) { return DP == 64 ? (row & 2) << 1 : (row & 3) << 2; }
+// The two shapes of a wave's products, v_mfma_f32_32x32x16 (R = 32 rows) and 16x16x32 (R = 16).
+template <int R> struct Shape;
+template <> struct Shape<32> {
+    typedef f32x16 acc;
+    static constexpr int kVals = 16, kDepth = 16;
+};
+template <> struct Shape<16> {
+    typedef f32x4 acc;
+    static constexpr int kVals = 4, kDepth = 32;
+};
+template <bool F16> __device__ __forceinline__ f32x16 product(op8<F16> a, op8<F16> b, f32x16 c) {
+    return mfma32x32x16<F16>(a, b, c);
+}
+template <bool F16> __device__ __forceinline__ f32x4 product(op8<F16> a, op8<F16> b, f32x4 c) {
+    return mfma16x16x32<F16>(a, b, c);
+}
 
 // float16 probabilities carry a factor 2^7 (which the division by their sum takes out again): their
 // smallest step is then 2^-31 of the largest, so long rows of small weights are not lost. With the
@@ -252,15 +291,17 @@ template <bool F16> constexpr float kLift = F16 ? 7.f : 0.f;
 // scales sums and probabilities alike, and most tiles then need no rescaling of the output sums.
 constexpr float kSlack = 8.f;
 
-template <bool F16, int DP, int NW, int KT>
+template <bool F16, int DP, int R, int NW, int KT>
 __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArgs a, Sched s) {
-    constexpr int ROWS = 32 * NW, NT = 64 * NW;
+    constexpr int ROWS = R * NW, NT = 64 * NW;
     constexpr int CH = DP / 8;               // 16-byte pieces of a row
     constexpr int PER = KT * CH / NT;        // pieces of a tile per thread, RSTEP rows apart
     constexpr int RSTEP = NT / CH;
-    constexpr int KB = KT / 32;
     constexpr int BUF = NW > 1 ? 2 : 1;
     constexpr int TILE = KT * DP;            // elements
+    constexpr int VALS = Shape<R>::kVals;    // a lane's values of a product
+    constexpr int QF = DP / Shape<R>::kDepth, SB = KT / R, PF = KT * R / 512, OB = DP / R;
+    typedef typename Shape<R>::acc acc_t;
     __shared__ __align__(16) uint16_t lds[BUF][2][TILE];
 
     const int hk = blockIdx.x % a.kv_heads;
@@ -269,11 +310,11 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
     if (!find_item<ROWS, KT>(a, s, item, false, it)) return;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int half = lane >> 5, col = lane & 31;
+    const int part = lane / R, col = lane % R;  // this lane's share of its row
     const int r0 = it.tile * ROWS;
     const int rows = min(ROWS, it.row_end - r0);
     // this lane's row
-    const int r = wave * 32 + col;
+    const int r = wave * R + col;
     const bool live = r < rows;
     const int token = (r0 + min(r, rows - 1)) / a.group;
     const int head = hk * a.group + (r0 + min(r, rows - 1)) - token * a.group;
@@ -290,53 +331,73 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
     // the wave's tiles below sure_hi and from sure_lo on need no mask; rows that are not there
     // need none either
     int sure_lo = live ? lo : 0, sure_hi = live ? hi : 0x7fffffff, any_hi = live ? hi : 0;
-    for (int x = 16; x > 0; x >>= 1) {
+    for (int x = R / 2; x > 0; x >>= 1) {
         sure_lo = max(sure_lo, __shfl_xor(sure_lo, x));
         sure_hi = min(sure_hi, __shfl_xor(sure_hi, x));
         any_hi = max(any_hi, __shfl_xor(any_hi, x));
     }
+    sure_lo = __builtin_amdgcn_readfirstlane(sure_lo);
+    sure_hi = __builtin_amdgcn_readfirstlane(sure_hi);
+    any_hi = __builtin_amdgcn_readfirstlane(any_hi);
 
-    // Q^T in registers: lane holds row `col`, values 16 c + 8 half ..
-    op8<F16> q[DP / 16];
+    // Q^T in registers: lane holds row `col`, values kDepth c + 8 part ..
+    op8<F16> q[QF];
     {
         const uint16_t* src = a.q + (int64_t)(it.start + token) * a.q_ts + (int64_t)head * a.q_hs;
 #pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-            const int d = 16 * c + 8 * half;
+        for (int c = 0; c < QF; ++c) {
+            const int d = Shape<R>::kDepth * c + 8 * part;
             u32x4a v = {0, 0, 0, 0};
             if (live && d < a.dim) v = *reinterpret_cast<const u32x4a*>(src + d);
             q[c] = __builtin_bit_cast(op8<F16>, v);
         }
     }
 
-    // staging: this thread's pieces are rows row0 + RSTEP i, piece `piece`
+    // Staging: this thread's pieces are rows row0 + RSTEP i of a tile, piece `piece`. A key's offset in
+    // its page is that of the tile's first key plus the row, or the row alone where pages are no longer
+    // than tiles: (kt * KT & page_mask) + (row & page_mask), the second part fixed.
     const int row0 = tid / CH, piece = tid % CH;
-    const bool piece_in = piece * 8 < a.dim;
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
-    const uint16_t* kc = a.k_cache + ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
-    const uint16_t* vc = a.v_cache + ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
+    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
+    const uint32_t stride = (uint32_t)a.page_stride;
+    const bool whole = a.dim == DP;
     int page[PER];
     u32x4a kreg[PER], vreg[PER];
     auto load_pages = [&](int kt) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int key = kt * KT + row0 + RSTEP * i;
-            page[i] = -1;
-            if (key < hi_all && (key >> a.page_shift) < a.table_width) page[i] = table[key >> a.page_shift];
+            const int entry = (kt * KT + row0 + RSTEP * i) >> a.page_shift;
+            // the last key's entry stands for those past it
+            page[i] = entry < a.table_width ? table[min(entry, (hi_all - 1) >> a.page_shift)] : -1;
         }
     };
     auto load_tile = [&](int kt) {
+        const int64_t tile_at = head_at + (int64_t)((kt * KT) & page_mask) * a.dim;
+        bool good = whole;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) good &= (uint32_t)page[i] < (uint64_t)a.pages;
+        if (kt * KT >= lo_all && (kt + 1) * KT <= hi_all && __all(good)) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + tile_at +
+                                    (uint32_t)(((row0 + RSTEP * i) & page_mask) * a.dim);
+                kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at);
+                vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int key = kt * KT + row0 + RSTEP * i;
+            const int row = row0 + RSTEP * i, key = kt * KT + row;
             u32x4a kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
             if (key >= lo_all && key < hi_all) {
                 if ((uint32_t)page[i] < (uint64_t)a.pages) {
-                    if (piece_in) {
-                        const int64_t at = page[i] * a.page_stride + (int64_t)(key & page_mask) * a.dim;
-                        kv = *reinterpret_cast<const u32x4a*>(kc + at);
-                        vv = *reinterpret_cast<const u32x4a*>(vc + at);
+                    if (piece * 8 < a.dim) {
+                        const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + tile_at +
+                                            (uint32_t)((row & page_mask) * a.dim);
+                        kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at);
+                        vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at);
                     }
                 } else {  // outside the pool: NaN scores, so the rows that see the key are NaN
                     kv = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
@@ -347,17 +408,18 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
         }
     };
 
-    f32x16 acc[DP / 32];
+    acc_t acc[OB];
 #pragma unroll
-    for (int n = 0; n < DP / 32; ++n)
+    for (int n = 0; n < OB; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[n][i] = 0.f;
+        for (int i = 0; i < VALS; ++i) acc[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;
+    bool redo = false;
     const float factor = a.scale * kLog2e;
 
-    // addresses of a lane's reads, in elements
-    const int v_row = 4 * half + ((lane & 15) >> 2);                          // + 16 c + 8 e + 32 kb
-    const int v_piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);            // + 4 n
+    // A lane's reads of V: rows 32 f' + kRow e + v_row, pieces (R / 8) n + v_piece, from value v_sub on.
+    const int v_row = 4 * part + ((lane & 15) >> 2);
+    const int v_piece = (R == 32 ? 2 * ((lane >> 4) & 1) : 0) + ((lane & 3) >> 1);
     const int v_sub = 4 * (lane & 1);
 
     if (kt_begin < kt_end) {
@@ -372,7 +434,7 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
         for (int i = 0; i < PER; ++i) {
             const int row = row0 + RSTEP * i;
             *reinterpret_cast<u32x4a*>(kl + row * DP + ((piece ^ swizzle_k<DP>(row)) * 8)) = kreg[i];
-            *reinterpret_cast<u32x4a*>(vl + row * DP + ((piece ^ swizzle_v<DP>(row)) * 8)) = vreg[i];
+            *reinterpret_cast<u32x4a*>(vl + row * DP + ((piece ^ swizzle_v<DP, R>(row)) * 8)) = vreg[i];
         }
         if (kt + 1 < kt_end) {
             load_tile(kt + 1);
@@ -383,122 +445,121 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
         const int key0 = kt * KT;
         if (key0 >= any_hi) continue;  // keys past every row of this wave
 
-        f32x16 sc[KB];
+        acc_t sc[SB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < SB; ++kb) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
+            for (int i = 0; i < VALS; ++i) sc[kb][i] = 0.f;
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) {
-                const int row = kb * 32 + col;
+            for (int c = 0; c < QF; ++c) {
+                const int row = kb * R + col;
                 const op8<F16> kf = *reinterpret_cast<const op8<F16>*>(
-                    kl + row * DP + (((2 * c + half) ^ swizzle_k<DP>(row)) * 8));
-                sc[kb] = mfma32x32x16<F16>(kf, q[c], sc[kb]);
+                    kl + row * DP + ((((Shape<R>::kDepth / 8) * c + part) ^ swizzle_k<DP>(row)) * 8));
+                sc[kb] = product<F16>(kf, q[c], sc[kb]);
             }
         }
-        const bool masked = key0 < sure_lo || key0 + KT > sure_hi;
-        if (masked) {
+        if (key0 < sure_lo || key0 + KT > sure_hi) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = key0 + kb * 32 + (i >> 2) * 8 + 4 * half + (i & 3);
+                for (int i = 0; i < VALS; ++i) {
+                    const int key = key0 + kb * R + (i >> 2) * 8 + 4 * part + (i & 3);
                     if (key < lo || key >= hi) sc[kb][i] = -INFINITY;
                 }
         }
         float top = sc[0][0];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
-        top = max_halves(top) * factor;
+            for (int i = 0; i < VALS; ++i) top = fmaxf(top, sc[kb][i]);
+        top = max_of_row<R>(top) * factor;
         if (__any(top > m + kSlack)) {
             const float m_new = fmaxf(m, top);
             const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
             l *= keep;
 #pragma unroll
-            for (int n = 0; n < DP / 32; ++n)
+            for (int n = 0; n < OB; ++n)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[n][i] *= keep;
+                for (int i = 0; i < VALS; ++i) acc[n][i] *= keep;
             m = m_new;
         }
         const float base = m == -INFINITY ? 0.f : m - kLift<F16>;
-        op8<F16> p[KB][2];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < VALS; ++i) {
                 sc[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[kb][i], factor, -base));
                 l += sc[kb][i];
             }
-            // rounded to 16 bits for the product with V; their sum l is taken before the rounding
+        // rounded to 16 bits for the product with V; their sum l is taken before the rounding
+        op8<F16> p[PF];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                p[kb][c] = __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(sc[kb][8 * c], sc[kb][8 * c + 1]),
-                                                               pack_half2<F16>(sc[kb][8 * c + 2], sc[kb][8 * c + 3]),
-                                                               pack_half2<F16>(sc[kb][8 * c + 4], sc[kb][8 * c + 5]),
-                                                               pack_half2<F16>(sc[kb][8 * c + 6], sc[kb][8 * c + 7])});
+        for (int f = 0; f < PF; ++f) {
+            float x[8];  // of one block of scores (two to a block), or of two blocks (R = 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = R == 32 ? sc[f / 2][8 * (f % 2) + i] : sc[2 * f + i / 4][i % 4];
+            p[f] = __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(x[0], x[1]), pack_half2<F16>(x[2], x[3]),
+                                                       pack_half2<F16>(x[4], x[5]), pack_half2<F16>(x[6], x[7])});
         }
         // A weight of zero times an infinite or NaN value is NaN: where the tile holds keys that some
-        // row does not see, look for such values, and keep them out of the products.
-        bool careful = false;
+        // row does not see, look for such values.
         if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) {
+#pragma unroll 1
             for (int x = lane; x < TILE / 8; x += 64) {
                 const u32x4a w = *reinterpret_cast<const u32x4a*>(vl + x * 8);
-                careful |= not_finite2<F16>(w.x) || not_finite2<F16>(w.y) || not_finite2<F16>(w.z) ||
-                           not_finite2<F16>(w.w);
+                redo |= not_finite2<F16>(w.x) || not_finite2<F16>(w.y) || not_finite2<F16>(w.z) || not_finite2<F16>(w.w);
             }
-            careful = __any(careful);
         }
 #pragma unroll
-        for (int n = 0; n < DP / 32; ++n) {
-            const int at = ((v_piece + 4 * n) ^ swizzle_v<DP>(v_row)) * 8 + v_sub;
+        for (int n = 0; n < OB; ++n) {
+            const int at = ((v_piece + (R / 8) * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint16_t* src = vl + (v_row + 32 * kb + 16 * c) * DP + at;
-                    const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
-                    const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + 8 * DP));
-                    const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
-                    u32x4a w = {w0.x, w0.y, w1.x, w1.y};
-                    if (careful)
-                        w = u32x4a{finite_or_zero2<F16>(w.x), finite_or_zero2<F16>(w.y), finite_or_zero2<F16>(w.z),
-                                   finite_or_zero2<F16>(w.w)};
-                    acc[n] = mfma32x32x16<F16>(__builtin_bit_cast(op8<F16>, w), p[kb][c], acc[n]);
-                }
-        }
-        if (careful) {  // what was kept out goes to the rows that see it, one key at a time
-            for (int j = 0; j < KT; ++j) {
-                const bool sees = key0 + j >= lo && key0 + j < hi;
-#pragma unroll
-                for (int n = 0; n < DP / 32; ++n)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int d = 32 * n + (i >> 2) * 8 + 4 * half + (i & 3);
-                        const uint32_t w = vl[j * DP + (((d >> 3) ^ swizzle_v<DP>(j)) * 8) + (d & 7)];
-                        if (sees && not_finite2<F16>(w)) acc[n][i] += half_to_f32<F16>(w);
-                    }
+            for (int f = 0; f < PF; ++f) {
+                uint16_t* src = vl + (v_row + (R == 32 ? 16 : 32) * f) * DP + at;
+                const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
+                const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + (R == 32 ? 8 : 16) * DP));
+                const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
+                acc[n] = product<F16>(__builtin_bit_cast(op8<F16>, u32x4a{w0.x, w0.y, w1.x, w1.y}), p[f], acc[n]);
             }
         }
     }
 
-    l = add_halves(l);
+    if (__any(redo)) {  // this wave's rows again, one by one, each over the keys that it sees alone
+#pragma unroll 1
+        for (int x = wave * R; x < min(wave * R + R, rows); ++x) {
+            const int i = (r0 + x) / a.group, h = hk * a.group + (r0 + x) - i * a.group;
+            int from, to;
+            seen_keys(a, it, i, from, to);
+            float mx, lx, o[4];
+            scalar_row<F16>(a, it.b, it.start + i, h, max(from, kt_begin * KT), min(to, kt_end * KT), mx, lx, o);
+            if (it.parts == 1) {
+                store_scalar_row<F16>(a, it.start + i, h, to <= from, mx, lx, o);
+                continue;
+            }
+            const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (lane + 64 * y < a.dim) s.part_o[slot * a.dim + lane + 64 * y] = o[y];
+            if (lane == 0) s.part_ml[slot] = make_float2(mx, lx);
+        }
+        return;
+    }
+    l = sum_of_row<R>(l);
     if (!live) return;
     const float m_out = m - kLift<F16>;
     if (it.parts > 1) {
         const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + r;
         float* o = s.part_o + slot * a.dim;
 #pragma unroll
-        for (int n = 0; n < DP / 32; ++n)
+        for (int n = 0; n < OB; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int d = 32 * n + 8 * i + 4 * half;
+            for (int i = 0; i < VALS / 4; ++i) {
+                const int d = R * n + 8 * i + 4 * part;
                 if (d < a.dim)
                     *reinterpret_cast<f32x4*>(o + d) =
                         f32x4{acc[n][4 * i], acc[n][4 * i + 1], acc[n][4 * i + 2], acc[n][4 * i + 3]};
             }
-        if (half == 0) s.part_ml[slot] = make_float2(m_out, l);
+        if (part == 0) s.part_ml[slot] = make_float2(m_out, l);
         return;
     }
     const bool empty = hi <= lo;
@@ -506,60 +567,77 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
     const int64_t row = (int64_t)(it.start + token) * a.heads + head;
     uint16_t* o = a.out + row * a.dim;
 #pragma unroll
-    for (int n = 0; n < DP / 32; ++n)
+    for (int n = 0; n < OB; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int d = 32 * n + 8 * i + 4 * half;
+        for (int i = 0; i < VALS / 4; ++i) {
+            const int d = R * n + 8 * i + 4 * part;
             if (d < a.dim)
                 *reinterpret_cast<uint2*>(o + d) = make_uint2(pack_half2<F16>(acc[n][4 * i] * inv, acc[n][4 * i + 1] * inv),
                                                               pack_half2<F16>(acc[n][4 * i + 2] * inv, acc[n][4 * i + 3] * inv));
         }
-    if (a.lse && half == 0) a.lse[row] = empty ? -INFINITY : (m_out + __builtin_amdgcn_logf(l)) * kLn2;
+    if (a.lse && part == 0) a.lse[row] = empty ? -INFINITY : (m_out + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // Joins the parts of a tile's rows, in their order: o = sum_s w_s o_s / sum_s w_s l_s with
-// w_s = 2^(m_s - max m). A workgroup takes one row of a tile at a time; DP / 4 threads hold the row
-// and the others take other parts.
-template <bool F16, int DP, int ROWS, int KT>
+// w_s = 2^(m_s - max m). A workgroup holds RP rows, DP / 4 threads each; the threads left over take
+// other parts of the same rows, up to kJoin parts at a time.
+constexpr int kJoin = 512;
+template <bool F16, int DP, int ROWS, int KT, int RP>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
-    constexpr int LANES = DP / 4, GROUPS = 256 / LANES;
+    constexpr int LANES = DP / 4, GROUPS = 256 / LANES / RP;
+    static_assert(GROUPS >= 1 && (RP == 1 || GROUPS == 1), "");
     __shared__ f32x4 so[GROUPS][LANES];
-    __shared__ float2 sml[GROUPS];
+    __shared__ float weight[RP][kJoin / RP];
     const int hk = blockIdx.x % a.kv_heads;
     Item it;
     if (!find_item<ROWS, KT>(a, s, blockIdx.x / a.kv_heads, true, it) || it.parts == 1) return;
-    const int x = threadIdx.x % LANES, g = threadIdx.x / LANES;
+    const int x = threadIdx.x % LANES, g = (threadIdx.x / LANES) % GROUPS, rp = threadIdx.x / (LANES * GROUPS);
     const int r0 = it.tile * ROWS, rows = min(ROWS, it.row_end - r0);
     const bool in = 4 * x < a.dim;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int lane_of_row = threadIdx.x % (LANES * GROUPS);
+    for (int rb = blockIdx.y * RP; rb < rows; rb += gridDim.y * RP) {
+        const int r = min(rb + rp, rows - 1);
+        const int64_t slot0 = ((int64_t)it.first * a.kv_heads + hk) * ROWS + r;
+        const int64_t step = (int64_t)a.kv_heads * ROWS;
         float m = -INFINITY, l = 0.f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int p = g; p < it.parts; p += GROUPS) {
-            const int64_t slot = ((int64_t)(it.first + p) * a.kv_heads + hk) * ROWS + r;
-            const float2 ml = s.part_ml[slot];
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (in) v = *reinterpret_cast<const f32x4*>(s.part_o + slot * a.dim + 4 * x);
-            const float m_new = fmaxf(m, ml.x);
-            const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float k0 = __builtin_amdgcn_exp2f(m - base), k1 = __builtin_amdgcn_exp2f(ml.x - base);
-            l = l * k0 + ml.y * k1;
-            o = o * k0 + v * k1;
-            m = m_new;
+        for (int p0 = 0; p0 < it.parts; p0 += kJoin / RP) {
+            const int n = min(kJoin / RP, it.parts - p0);
+            // this stretch's maximum and sum, by every wave for its own row
+            float top = m;
+            for (int p = threadIdx.x & (min(64, LANES * GROUPS) - 1); p < n; p += min(64, LANES * GROUPS))
+                top = fmaxf(top, s.part_ml[slot0 + (p0 + p) * step].x);
+            for (int y = min(64, LANES * GROUPS) / 2; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor(top, y));
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            __syncthreads();
+            for (int p = threadIdx.x & (min(64, LANES * GROUPS) - 1); p < n; p += min(64, LANES * GROUPS)) {
+                const float2 ml = s.part_ml[slot0 + (p0 + p) * step];
+                const float w = __builtin_amdgcn_exp2f(ml.x - base);
+                sum += w * ml.y;
+                if (lane_of_row < 64) weight[rp][p] = w;
+            }
+            for (int y = min(64, LANES * GROUPS) / 2; y > 0; y >>= 1) sum += __shfl_xor(sum, y);
+            __syncthreads();
+            const float keep = __builtin_amdgcn_exp2f(m - base);
+            l = l * keep + sum;
+            o *= keep;
+            m = top;
+            if (in) {
+                const float* src = s.part_o + (slot0 + (int64_t)p0 * step) * a.dim + 4 * x;
+#pragma unroll 8
+                for (int p = g; p < n; p += GROUPS)
+                    o += weight[rp][p] * *reinterpret_cast<const f32x4*>(src + p * step * a.dim);
+            }
         }
-        __syncthreads();
-        so[g][x] = o;
-        if (x == 0) sml[g] = make_float2(m, l);
-        __syncthreads();
-        if (g != 0) continue;
-        for (int p = 1; p < GROUPS; ++p) {
-            const float2 ml = sml[p];
-            const float m_new = fmaxf(m, ml.x);
-            const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float k0 = __builtin_amdgcn_exp2f(m - base), k1 = __builtin_amdgcn_exp2f(ml.x - base);
-            l = l * k0 + ml.y * k1;
-            o = o * k0 + so[p][x] * k1;
-            m = m_new;
+        if (GROUPS > 1) {
+            __syncthreads();
+            so[g][x] = o;
+            __syncthreads();
+            if (g == 0)
+                for (int p = 1; p < GROUPS; ++p) o += so[p][x];
         }
+        if (g != 0 || rb + rp >= rows) continue;
         const int token = (r0 + r) / a.group, head = hk * a.group + (r0 + r) - token * a.group;
         int lo, hi;
         seen_keys(a, it, token, lo, hi);
@@ -573,8 +651,12 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
     }
 }
 
-// How a call runs: the few-rows kernel (32-row tiles), the many-rows kernel (128-row tiles) or both,
-// and whether their tiles are cut along the keys.
+// How a call runs: the few-rows kernel (16-row tiles), the many-rows kernel (tiles of kManyRows) or
+// both, and whether their tiles are cut along the keys.
+constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
+constexpr int kFewMax = 32;  // requests of more rows are the many-rows kernel's
+constexpr int kFewPart = 2, kManyPart = 8;
+
 struct Launches {
     struct One {
         int64_t tiles = 0;  // at most so many tiles (0: not launched)
@@ -585,32 +667,31 @@ struct Launches {
     } few, many;
 };
 
-Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
-                       int64_t requests, int64_t max_new) {
+Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t table_keys, int64_t requests,
+                       int64_t max_new) {
     Launches p;
     const int64_t group = heads / kv_heads, rows = tokens * group, cus = device_cu_count();
     const int64_t holders = requests + 1 < tokens ? requests + 1 : tokens;  // requests with rows
-    const bool one = requests == 1 && rows > 32;
-    if (max_new * group <= 32 || rows <= 32) {
-        p.few.tiles = holders + rows / 32;
+    if (max_new <= kFewMax / group || rows <= kFewMax) {
+        p.few.tiles = holders + rows / 16;
         p.few.rows_hi = 0x7fffffff;
     } else {
-        if (!one) {
-            p.few.tiles = holders;
-            p.few.rows_hi = 32;
-            p.many.rows_lo = 32;
+        if (requests > 1) {
+            p.few.tiles = 2 * holders;
+            p.few.rows_hi = kFewMax;
+            p.many.rows_lo = kFewMax;
         }
-        p.many.tiles = rows / 128 + (holders < rows / 33 + 1 ? holders : rows / 33 + 1);
+        const int64_t large = rows / (kFewMax + 1) + 1;
+        p.many.tiles = rows / kManyRows + (holders < large ? holders : large);
         p.many.rows_hi = 0x7fffffff;
     }
-    p.few.rows = 32;
-    p.many.rows = 128;
+    p.few.rows = 16;
+    p.many.rows = kManyRows;
     // Cut where whole tiles would leave workgroup slots empty: 8 waves of the few-rows kernel fit a
-    // CU, 2 workgroups of the other. Parts have 4 (2) times the slots, so that uneven ends are short.
-    if (p.few.tiles && table_keys > 32 * kMinPart) p.few.parts = (int)((cus * 16 + kv_heads - 1) / kv_heads);
+    // CU, 2 workgroups of the other. Twice as many parts, so that uneven ends are short.
+    if (p.few.tiles && table_keys > 32 * kFewPart) p.few.parts = (int)((cus * 16 + kv_heads - 1) / kv_heads);
     const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
-    if (p.many.tiles && p.many.tiles < slots && table_keys > 64 * kMinPart) p.many.parts = (int)(2 * slots);
-    (void)head_dim;
+    if (p.many.tiles && p.many.tiles < slots && table_keys > 64 * kManyPart) p.many.parts = (int)(2 * slots);
     return p;
 }
 
@@ -620,16 +701,19 @@ hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream
     const size_t few_slots = p.few.slots(a.kv_heads), many_slots = p.many.slots(a.kv_heads);
     float* o = a.partial;
     float2* ml = reinterpret_cast<float2*>(o + (few_slots + many_slots) * a.dim);
-    const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, o, ml};
-    const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, o + few_slots * a.dim, ml + few_slots};
+    const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, kFewPart, o, ml};
+    const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, kManyPart * 64 / KT, o + few_slots * a.dim,
+                     ml + few_slots};
     if (p.many.tiles)
-        attn_kernel<F16, DP, 4, KT><<<(unsigned)(p.many.items() * a.kv_heads), 256, 0, stream>>>(a, many);
-    if (p.few.tiles) attn_kernel<F16, DP, 1, 32><<<(unsigned)(p.few.items() * a.kv_heads), 64, 0, stream>>>(a, few);
+        attn_kernel<F16, DP, 32, kManyWaves, KT>
+            <<<(unsigned)(p.many.items() * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
+    if (p.few.tiles) attn_kernel<F16, DP, 16, 1, 32><<<(unsigned)(p.few.items() * a.kv_heads), 64, 0, stream>>>(a, few);
     if (p.many.parts)
-        join_kernel<F16, DP, 128, KT><<<dim3((unsigned)(p.many.tiles * a.kv_heads), 64), 256, 0, stream>>>(a, many);
+        join_kernel<F16, DP, kManyRows, KT, 1024 / DP>
+            <<<dim3((unsigned)(p.many.tiles * a.kv_heads), kManyRows / (1024 / DP)), 256, 0, stream>>>(a, many);
     if (p.few.parts)
-        join_kernel<F16, DP, 32, 32>
-            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < 32 ? a.group : 32), 256, 0, stream>>>(a, few);
+        join_kernel<F16, DP, 16, 32, 1>
+            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < 16 ? a.group : 16), 256, 0, stream>>>(a, few);
     return hipGetLastError();
 }
 
@@ -639,13 +723,14 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 size_t paged_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
                                  int64_t requests, int64_t max_new) {
-    const Launches p = plan_launches(tokens, heads, kv_heads, head_dim, table_keys, requests, max_new);
+    const Launches p = plan_launches(tokens, heads, kv_heads, table_keys, requests, max_new);
     return (p.few.slots(kv_heads) + p.many.slots(kv_heads)) * (size_t)(4 * head_dim + 8);
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, hipStream_t stream) {
-    // 16-byte loads of every row, and heads of whole 16-byte pieces
+    // 16-byte loads of every row, and heads of whole 16-byte pieces (pages apart by a 32-bit count)
     const bool pieces = a.dim % 8 == 0 && a.q_ts % 8 == 0 && a.q_hs % 8 == 0 && a.page_stride % 8 == 0 &&
+                        a.page_stride < (1LL << 32) &&
                         aligned16(a.q) && aligned16(a.k_cache) && aligned16(a.v_cache) && aligned16(a.out);
     if (!pieces) {
         const unsigned grid = (unsigned)a.tokens * (unsigned)a.heads;
@@ -653,7 +738,7 @@ hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, 
         else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_width << a.page_shift, a.requests, max_new);
+    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.table_width << a.page_shift, a.requests, max_new);
     if (a.dim <= 64) return f16 ? launch_tiles<true, 64>(a, p, stream) : launch_tiles<false, 64>(a, p, stream);
     if (a.dim <= 128) return f16 ? launch_tiles<true, 128>(a, p, stream) : launch_tiles<false, 128>(a, p, stream);
     return f16 ? launch_tiles<true, 256>(a, p, stream) : launch_tiles<false, 256>(a, p, stream);
