@@ -53,7 +53,7 @@ qaff_status bad_page_size(const char* op, int32_t page_size) {
     return fail(QAFF_ERR_UNSUPPORTED, "%s: page size %d is not supported (8, 16, 32, 64, 128 or 256)", op, page_size);
 }
 
-constexpr int64_t k2G = 1LL << 31;
+constexpr int64_t k1G = 1LL << 30, k2G = 1LL << 31;
 
 // The caches' sizes: every page holds kv_heads * page_size * head_dim elements, page_stride apart.
 qaff_status check_cache(const char* op, int64_t pages, int64_t page_stride, int64_t kv_heads, int64_t head_dim,
@@ -204,7 +204,7 @@ size_t qaff_paged_attention_workspace_size(int64_t tokens, int64_t heads, int64_
                                            int64_t max_new) {
     if (tokens <= 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || head_dim <= 0 || head_dim > 256 ||
         requests <= 0 || requests > 65536 || table_width <= 0 || page_shift_of(page_size) < 0 ||
-        tokens >= k2G / heads || table_width >= k2G / page_size)
+        tokens >= k2G / heads || table_width >= k1G / page_size)
         return 0;
     return qaff::paged_attention_workspace(tokens, heads, kv_heads, head_dim, table_width * page_size, requests, max_new);
 }
@@ -233,8 +233,8 @@ qaff_status qaff_paged_attention(const void* q, qaff_dtype dtype, int64_t tokens
     if (requests > 65536) return fail(QAFF_ERR_UNSUPPORTED, "%s: more than 65536 requests", op);
     if (heads > 0 && tokens >= k2G / heads)
         return fail(QAFF_ERR_UNSUPPORTED, "%s: %lld tokens of %lld heads", op, (long long)tokens, (long long)heads);
-    if (table_width >= k2G / page_size)
-        return fail(QAFF_ERR_UNSUPPORTED, "%s: a table of %lld pages is 2^31 tokens or more", op, (long long)table_width);
+    if (table_width >= k1G / page_size)
+        return fail(QAFF_ERR_UNSUPPORTED, "%s: a table of %lld pages is 2^30 tokens or more", op, (long long)table_width);
     if (!(scale > 0.f) || !std::isfinite(scale))
         return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: scale %g is not positive and finite", op, (double)scale);
     qaff_status st = check_cache(op, pages, page_stride, kv_heads, head_dim, page_size);
@@ -274,6 +274,7 @@ qaff_status qaff_paged_attention(const void* q, qaff_dtype dtype, int64_t tokens
     a.q_hs = q_head_stride;
     a.page_stride = page_stride;
     a.table_width = table_width;
+    a.table_keys = (int)(table_width * page_size);
     a.pages = pages;
     a.window = window;
     a.tokens = (int)tokens;

@@ -50,6 +50,7 @@ struct AttnArgs {
     float* partial;  // workspace
     int64_t q_ts, q_hs, page_stride, table_width, pages, window;  // window 0: none
     int tokens, heads, kv_heads, group, dim, page_shift, requests, causal;
+    int table_keys;  // table_width pages of keys
     float scale;
 };
 hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, hipStream_t stream);

@@ -101,6 +101,11 @@ __global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
         const int64_t pos = kv - a.cu[b + 1] + t;
         hi = a.causal ? min(kv, pos + 1) : kv;
         lo = a.window > 0 ? max((int64_t)0, pos - a.window + 1) : 0;
+        // keys past the table make the row NaN, and one of them is enough
+        if (hi > a.table_keys + 1) {
+            hi = a.table_keys + 1;
+            lo = min(lo, (int64_t)a.table_keys);
+        }
     }
     float m, l, acc[4];
     scalar_row<F16>(a, b, t, h, lo, hi, m, l, acc);
@@ -119,13 +124,13 @@ __global__ __launch_bounds__(64) void attn_scalar_kernel(AttnArgs a) {
 // wants of P^T, if the 16 keys of a product are numbered as they lie: half h holds keys 4 h .. 4 h + 3
 // and 8 + 4 h .. 8 + 4 h + 3 of each 16, and the reads of V^T take the same order.
 //
-// NW waves make a workgroup of 32 NW rows: NW = 4 for chunks and prompts (keys staged once for 128
-// rows), NW = 1 where a request has at most 32 rows (decode), there with the keys of a request split
-// over as many workgroups as fill the chip.
+// Two kernels share this. Chunks and prompts: 4 waves of 32 rows, K and V tiles of 64 keys staged once
+// for the 128 rows. A few rows (decode): every wave of a workgroup takes all rows, at most 16, and other
+// keys, with v_mfma_f32_16x16x32; the waves join in LDS. Where tiles are few, both cut a tile's keys
+// into parts for several workgroups, and a second kernel joins those.
 //
-// K and V tiles go through registers into LDS one tile ahead. LDS holds 16-byte pieces, piece c of
-// row r at c ^ f(r), so that neither the row-wise reads of K nor the transposing reads of V (4 rows
-// by 64 bytes for half a wave) meet in a bank.
+// LDS holds 16-byte pieces, piece c of row r at c ^ f(r), so that neither the row-wise reads of K nor
+// the transposing reads of V (4 rows by 64 bytes, or 8 by 32, for half a wave) meet in a bank.
 
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -149,85 +154,119 @@ struct Item {
 };
 
 
+// One step of a scan in registers (no LDS round trip): v of the lane that the DPP control names, 0
+// where that lane is not there.
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+// Inclusive sums over the wave's lanes: within rows of 16 lanes (row_shr 1, 2, 4, 8), then the last
+// lane of a row to the next rows (row_bcast 15 and 31).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp<0x111, 0xf>(v);
+    v += dpp<0x112, 0xf>(v);
+    v += dpp<0x114, 0xf>(v);
+    v += dpp<0x118, 0xf>(v);
+    v += dpp<0x142, 0xa>(v);
+    v += dpp<0x143, 0xc>(v);
+    return v;
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
 // Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
 // Every wave scans the requests itself, 64 at a time: with up to 63 requests that is one load of
-// each length and a few cross-lane sums, less than reading another kernel's schedule would cost.
-// Rows past the last request are one more request without keys.
+// each length and two scans, less than reading another kernel's schedule would cost. Rows past the
+// last request are one more request without keys.
 template <int ROWS, int KT>
-__device__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_tile, Item& it) {
+__device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_tile, Item& it) {
     const int lane = threadIdx.x & 63;
     const int count = a.requests + 1;
-    const int per_tile = ROWS / a.group + 2;  // tokens a tile may touch
     int start = 0, end = 0, kv = 0, tiles = 0, span = 0;
     auto load = [&](int b) {
         start = end = kv = tiles = span = 0;
         if (b < a.requests) {
             start = a.cu[b];
             end = a.cu[b + 1];
-            kv = max(a.kv_lens[b], 0);
+            kv = a.kv_lens[b];
         } else if (b == a.requests) {
             start = a.cu[b];
             end = a.tokens;
         }
+        kv = max(kv, 0);
         if (start >= 0 && end > start && end <= a.tokens) {
-            const int64_t rows = (int64_t)(end - start) * a.group;
-            if (rows > s.rows_lo && rows <= s.rows_hi) tiles = (int)((rows + ROWS - 1) / ROWS);
+            const int rows = (end - start) * a.group;  // at most tokens * heads < 2^31
+            if (rows > s.rows_lo && rows <= s.rows_hi) tiles = (int)(((uint32_t)rows + ROWS - 1) / ROWS);
         }
-        int64_t keys = kv;
-        if (a.window > 0) keys = min(keys, a.window + per_tile + KT);
-        span = (int)((keys + KT - 1) / KT);
+        // key tiles that a tile's rows see: all, or with a window that and the tokens a tile may touch
+        const uint32_t window = (uint32_t)min(a.window, (int64_t)0x3fffffff) + (uint32_t)(ROWS / a.group + 2 + KT);
+        const uint32_t keys = a.window > 0 ? min((uint32_t)kv, window) : (uint32_t)kv;
+        span = (int)((min(keys, (uint32_t)a.table_keys) + KT - 1) / KT);
     };
     load(lane);
-    int64_t len = 1LL << 40;  // key tiles a part has
+    uint32_t len = 0x7fffffffu;  // key tiles of a part
     if (s.parts > 0) {
-        int64_t total = (int64_t)tiles * span;
+        // tiles times spans; where 32 bits might not hold the sum, nothing is cut
+        const uint32_t cap = 0x7fffffffu / (uint32_t)count;
+        bool past_cap = false;
+        auto product = [&] {
+            const uint64_t x = (uint64_t)(uint32_t)tiles * (uint32_t)span;
+            past_cap |= x > cap;
+            return (int)min(x, (uint64_t)cap);
+        };
+        int total = product();
         for (int b0 = 64; b0 < count; b0 += 64) {
             load(b0 + lane);
-            total += (int64_t)tiles * span;
+            total += product();
         }
-        for (int x = 32; x > 0; x >>= 1) total += __shfl_xor(total, x);
-        len = max((int64_t)s.min_part, (total + s.parts - 1) / s.parts);
+        const uint32_t all = (uint32_t)lane_value(wave_scan(total), 63);
+        if (!__any(past_cap)) len = max((uint32_t)s.min_part, (all + (uint32_t)s.parts - 1) / (uint32_t)s.parts);
         if (count > 64) load(lane);
     }
     int items_before = 0, tiles_before = 0;
     for (int b0 = 0;; b0 += 64) {
-        const int parts = max(1, (int)((span + len - 1) / len));
+        const int parts = max(1, (int)(((uint32_t)span + len - 1) / len));
         const int items = tiles * parts;
-        int items_in = items, tiles_in = tiles;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(items_in, d), w = __shfl_up(tiles_in, d);
-            if (lane >= d) items_in += u, tiles_in += w;
-        }
-        const int upto = by_tile ? tiles_before + tiles_in : items_before + items_in;
-        const uint64_t past = __ballot(upto > want);
+        const int items_in = items_before + wave_scan(items), tiles_in = tiles_before + wave_scan(tiles);
+        const uint64_t past = __ballot((by_tile ? tiles_in : items_in) > want);
         if (past) {
             const int at = __builtin_ctzll(past);
-            const int base = __shfl(items_before + items_in - items, at);
-            const int n = __shfl(parts, at), t = __shfl(tiles, at);
-            const int local = by_tile ? want - __shfl(tiles_before + tiles_in - tiles, at) : (want - base) / n;
+            const int base = lane_value(items_in - items, at);
+            const int n = lane_value(parts, at), t = lane_value(tiles, at);
+            const int local = by_tile ? want - lane_value(tiles_in - tiles, at) : (int)((uint32_t)(want - base) / (uint32_t)n);
             it.first = base + local * n;
             it.part = by_tile ? 0 : want - it.first;
             it.parts = n;
             it.tile = t - 1 - local;  // a causal prompt's last rows see the most keys: they go first
-            it.start = __shfl(start, at);
-            it.end = __shfl(end, at);
-            it.kv = __shfl(kv, at);
+            it.start = lane_value(start, at);
+            it.end = lane_value(end, at);
+            it.kv = lane_value(kv, at);
             it.row_end = (it.end - it.start) * a.group;
             it.b = b0 + at;
             return true;
         }
-        items_before += __shfl(items_in, 63);
-        tiles_before += __shfl(tiles_in, 63);
+        items_before = lane_value(items_in, 63);
+        tiles_before = lane_value(tiles_in, 63);
         if (b0 + 64 >= count) return false;
         load(b0 + 64 + lane);
     }
 }
 
-// The keys [lo, hi) that token i of the request sees.
+// Key tiles [begin, end) of an item's part, of n from tile t0 on: the first n % parts are one longer.
+__device__ __forceinline__ void part_of(const Item& it, int t0, int n, int& begin, int& end) {
+    const int each = (int)((uint32_t)n / (uint32_t)it.parts), more = n - each * it.parts;
+    begin = t0 + it.part * each + min(it.part, more);
+    end = begin + each + (it.part < more ? 1 : 0);
+}
+
+// The keys [lo, hi) that token i of the request sees. Keys past the table make the row NaN, and one
+// of them is enough: a length beyond the table must not keep the loops busy.
 __device__ __forceinline__ void seen_keys(const AttnArgs& a, const Item& it, int i, int& lo, int& hi) {
     const int pos = it.kv - (it.end - it.start) + i;
     hi = a.causal ? max(0, min(it.kv, pos + 1)) : it.kv;
     lo = a.window > 0 ? (int)max((int64_t)0, pos + 1 - a.window) : 0;
+    if (hi > a.table_keys + 1) {
+        hi = a.table_keys + 1;
+        lo = min(lo, a.table_keys);
+    }
 }
 
 // The maximum and the sum of v over the lanes that hold the same row: lane and lane ^ 32, and with 16
@@ -270,11 +309,11 @@ template <int DP, int R> __device__ __forceinline__ int swizzle_v(int row) {
 template <int R> struct Shape;
 template <> struct Shape<32> {
     typedef f32x16 acc;
-    static constexpr int kVals = 16, kDepth = 16;
+    static constexpr int kVals = 16;
 };
 template <> struct Shape<16> {
     typedef f32x4 acc;
-    static constexpr int kVals = 4, kDepth = 32;
+    static constexpr int kVals = 4;
 };
 template <bool F16> __device__ __forceinline__ f32x16 product(op8<F16> a, op8<F16> b, f32x16 c) {
     return mfma32x32x16<F16>(a, b, c);
@@ -291,18 +330,317 @@ template <bool F16> constexpr float kLift = F16 ? 7.f : 0.f;
 // scales sums and probabilities alike, and most tiles then need no rescaling of the output sums.
 constexpr float kSlack = 8.f;
 
-template <bool F16, int DP, int R, int NW, int KT>
-__global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArgs a, Sched s) {
-    constexpr int ROWS = R * NW, NT = 64 * NW;
+// Keys outside [lo, hi) of the lane's row out of a tile's scores. Value i of block kb is key
+// R kb + 8 (i / 4) + 4 part + i % 4 of the tile.
+template <int R, int SB>
+__device__ __forceinline__ void mask_scores(typename Shape<R>::acc (&sc)[SB], int key0, int part, int lo, int hi) {
+    asm volatile("");  // keeps the caller's branch: few tiles need this, and selects would cost all of them
+#pragma unroll
+    for (int kb = 0; kb < SB; ++kb)
+#pragma unroll
+        for (int i = 0; i < Shape<R>::kVals; ++i) {
+            const int key = key0 + kb * R + (i >> 2) * 8 + 4 * part + (i & 3);
+            if (key < lo || key >= hi) sc[kb][i] = -INFINITY;
+        }
+}
+
+// One tile of the running softmax: scores to probabilities (of the stale maximum), their sum into l,
+// and the output sums to a new maximum where the old one is passed by more than the slack.
+template <bool F16, int R, int SB, int OB>
+__device__ __forceinline__ void softmax_tile(typename Shape<R>::acc (&sc)[SB], typename Shape<R>::acc (&acc)[OB],
+                                             float factor, float& m, float& l) {
+    float top = sc[0][0];
+#pragma unroll
+    for (int kb = 0; kb < SB; ++kb)
+#pragma unroll
+        for (int i = 0; i < Shape<R>::kVals; ++i) top = fmaxf(top, sc[kb][i]);
+    top = max_of_row<R>(top) * factor;
+    if (__any(top > m + kSlack)) {
+        const float m_new = fmaxf(m, top);
+        const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+        l *= keep;
+#pragma unroll
+        for (int n = 0; n < OB; ++n)
+#pragma unroll
+            for (int i = 0; i < Shape<R>::kVals; ++i) acc[n][i] *= keep;
+        m = m_new;
+    }
+    const float base = m == -INFINITY ? 0.f : m - kLift<F16>;
+#pragma unroll
+    for (int kb = 0; kb < SB; ++kb)
+#pragma unroll
+        for (int i = 0; i < Shape<R>::kVals; ++i) {
+            sc[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[kb][i], factor, -base));
+            l += sc[kb][i];
+        }
+}
+
+// Eight probabilities rounded to 16 bits for their product with V (their sum l is taken before).
+template <bool F16, typename V0, typename V1>
+__device__ __forceinline__ op8<F16> pack8(V0 a, V1 b) {
+    return __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(a[0], a[1]), pack_half2<F16>(a[2], a[3]),
+                                               pack_half2<F16>(b[0], b[1]), pack_half2<F16>(b[2], b[3])});
+}
+
+// Two transposing reads: 4 + 4 values of one column of V (see the layouts above) as an operand.
+template <bool F16>
+__device__ __forceinline__ op8<F16> read_column(uint16_t* p0, uint16_t* p1) {
+    const u32x2 w0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p0));
+    const u32x2 w1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p1));
+    return __builtin_bit_cast(op8<F16>, u32x4a{w0.x, w0.y, w1.x, w1.y});
+}
+
+// Whether the lane's share of a tile of V in LDS holds an infinite or NaN value.
+template <bool F16, int PIECES>
+__device__ __forceinline__ bool tile_not_finite(const uint16_t* vl) {
+    bool found = false;
+#pragma unroll 1
+    for (int x = threadIdx.x & 63; x < PIECES; x += 64) {
+        const u32x4a w = *reinterpret_cast<const u32x4a*>(vl + x * 8);
+        found |= not_finite2<F16>(w.x) || not_finite2<F16>(w.y) || not_finite2<F16>(w.z) || not_finite2<F16>(w.w);
+    }
+    return found;
+}
+
+// A weight of zero times an infinite or NaN value is NaN. Where a tile holds keys that some row does not
+// see and such a value, the rows [x0, x1) of the item's tile are taken again, one by one, each over the
+// keys that it sees alone. Rare, and kept out of the loops, whose registers it would cost.
+template <bool F16, int ROWS>
+__device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& it, int item, int hk, int x0, int x1,
+                                int step, int key_begin, int key_end) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll 1
+    for (int x = x0; x < x1; x += step) {
+        const int r = it.tile * ROWS + x, i = r / a.group, h = hk * a.group + r - i * a.group;
+        int from, to;
+        seen_keys(a, it, i, from, to);
+        float mx, lx, o[4];
+        scalar_row<F16>(a, it.b, it.start + i, h, max(from, key_begin), min(to, key_end), mx, lx, o);
+        if (it.parts == 1) {
+            store_scalar_row<F16>(a, it.start + i, h, to <= from, mx, lx, o);
+            continue;
+        }
+        const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + x;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            if (lane + 64 * y < a.dim) s.part_o[slot * a.dim + lane + 64 * y] = o[y];
+        if (lane == 0) s.part_ml[slot] = make_float2(mx, lx);
+    }
+}
+
+// A few rows: NS waves, each with the tile's (at most 16) rows and every NS-th tile of 32 keys, no
+// barrier in the loop. K is read from memory as the product wants it: 16 rows of 64 bytes an
+// instruction, a lane's 2 rows the same for K and V, so a tile costs it 2 table lookups and 2
+// addresses. A tile's keys are used before its values: their registers take the next tile's loads
+// at once, so a wave has about a tile (16 KB at 128 values) in flight all the time.
+constexpr int kFewRows = 16;
+template <bool F16, int DP, int NS>
+__global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(AttnArgs a, Sched s) {
+    constexpr int KT = 32, R = 16;
+    constexpr int QF = DP / 32, OB = DP / 16;
+    constexpr int BYTES = KT * DP * 2;  // of a wave: V's tile, then its rows' sums (16 rows of DP floats)
+    __shared__ __align__(16) uint8_t lds[NS][BYTES];
+    __shared__ float2 ml[NS][R];
+
+    const int hk = blockIdx.x % a.kv_heads;
+    const int item = blockIdx.x / a.kv_heads;
+    Item it;
+    if (!find_item<R, KT>(a, s, item, false, it)) return;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int part = lane >> 4, col = lane & 15;
+    const int r0 = it.tile * R;
+    const int rows = min(R, it.row_end - r0);
+    const bool live = col < rows;
+    const int token = (r0 + min(col, rows - 1)) / a.group;
+    const int head = hk * a.group + (r0 + min(col, rows - 1)) - token * a.group;
+    int lo, hi;
+    seen_keys(a, it, token, lo, hi);
+    int lo_all, hi_all, unused;
+    seen_keys(a, it, r0 / a.group, lo_all, unused);
+    seen_keys(a, it, (r0 + rows - 1) / a.group, unused, hi_all);
+    const int kt0 = lo_all / KT;
+    const int n_all = max(0, (hi_all + KT - 1) / KT - kt0);
+    int kt_begin, kt_end;
+    part_of(it, kt0, n_all, kt_begin, kt_end);
+    // the first token sees the least far back keys, the last the farthest: between, no mask is needed
+    int sure_lo, sure_hi;
+    seen_keys(a, it, (r0 + rows - 1) / a.group, sure_lo, unused);
+    seen_keys(a, it, r0 / a.group, unused, sure_hi);
+
+    const int page_mask = (1 << a.page_shift) - 1;
+    const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
+    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim + part * 8;
+    const uint32_t stride = (uint32_t)a.page_stride;
+    const bool whole = a.dim == DP;
+    int page[2];
+    u32x4a kreg[2][QF], vreg[2][QF];
+    auto load_pages = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int entry = (kt * KT + 16 * i + col) >> a.page_shift;
+            // the last key's entry stands for those past it
+            page[i] = entry < a.table_width ? table[min(entry, (hi_all - 1) >> a.page_shift)] : -1;
+        }
+    };
+    auto load_tile = [&](int kt) {
+        const bool good = (uint32_t)page[0] < (uint64_t)a.pages && (uint32_t)page[1] < (uint64_t)a.pages;
+        if (whole && kt * KT >= lo_all && (kt + 1) * KT <= hi_all && __all(good)) {
+            uint64_t at[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                at[i] = (uint64_t)(uint32_t)page[i] * stride + head_at + (uint32_t)(((kt * KT + 16 * i + col) & page_mask) * DP);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < QF; ++c) kreg[i][c] = *reinterpret_cast<const u32x4a*>(a.k_cache + at[i] + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < QF; ++c) vreg[i][c] = *reinterpret_cast<const u32x4a*>(a.v_cache + at[i] + 32 * c);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = kt * KT + 16 * i + col;
+            const bool in = key >= lo_all && key < hi_all, ok = (uint32_t)page[i] < (uint64_t)a.pages;
+            const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + head_at + (uint32_t)((key & page_mask) * a.dim);
+            // outside the pool: NaN scores, so the rows that see the key are NaN
+            const uint32_t none = in && !ok ? 0x7FFF7FFFu : 0u;
+#pragma unroll
+            for (int c = 0; c < QF; ++c) {
+                u32x4a kv = {none, none, none, none}, vv = {0, 0, 0, 0};
+                if (in && ok && 32 * c + 8 * part < a.dim) {
+                    kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at + 32 * c);
+                    vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at + 32 * c);
+                }
+                kreg[i][c] = kv;
+                vreg[i][c] = vv;
+            }
+        }
+    };
+
+    int kt = kt_begin + wave;
+    if (kt < kt_end) {
+        load_pages(kt);
+        load_tile(kt);
+        load_pages(kt + NS);
+    }
+    // Q^T in registers: lane holds row `col`, values 32 c + 8 part ..
+    op8<F16> q[QF];
+    {
+        const uint16_t* src = a.q + (int64_t)(it.start + token) * a.q_ts + (int64_t)head * a.q_hs;
+#pragma unroll
+        for (int c = 0; c < QF; ++c) {
+            u32x4a v = {0, 0, 0, 0};
+            if (live && 32 * c + 8 * part < a.dim) v = *reinterpret_cast<const u32x4a*>(src + 32 * c + 8 * part);
+            q[c] = __builtin_bit_cast(op8<F16>, v);
+        }
+    }
+    f32x4 acc[OB];
+#pragma unroll
+    for (int n = 0; n < OB; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+    bool again = false;
+    const float factor = a.scale * kLog2e;
+    uint16_t* vl = reinterpret_cast<uint16_t*>(lds[wave]);
+    // a lane's transposing reads: rows v_row and v_row + 16, pieces 2 n + v_piece, from value v_sub on
+    const int v_row = 4 * part + (col >> 2), v_piece = (lane & 3) >> 1, v_sub = 4 * (lane & 1);
+
+    for (; kt < kt_end; kt += NS) {
+        f32x4 sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            sc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < QF; ++c) sc[i] = product<F16>(__builtin_bit_cast(op8<F16>, kreg[i][c]), q[c], sc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < QF; ++c) {
+                const int row = 16 * i + col;
+                *reinterpret_cast<u32x4a*>(vl + row * DP + (((4 * c + part) ^ swizzle_v<DP, R>(row)) * 8)) = vreg[i][c];
+            }
+        if (kt + NS < kt_end) {
+            load_tile(kt + NS);
+            load_pages(kt + 2 * NS);
+        }
+        const int key0 = kt * KT;
+        if (key0 < sure_lo || key0 + KT > sure_hi) {
+            mask_scores<R>(sc, key0, part, lo, hi);
+            if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) again |= tile_not_finite<F16, KT * DP / 8>(vl);
+        }
+        softmax_tile<F16, R>(sc, acc, factor, m, l);
+        const op8<F16> p = pack8<F16>(sc[0], sc[1]);
+#pragma unroll
+        for (int n = 0; n < OB; ++n) {
+            uint16_t* src = vl + v_row * DP + ((v_piece + 2 * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
+            acc[n] = product<F16>(read_column<F16>(src, src + 16 * DP), p, acc[n]);
+        }
+    }
+
+    l = sum_of_row<R>(l);
+    if (__syncthreads_or(again)) {
+        take_rows_again<F16, R>(a, s, it, item, hk, wave, rows, NS, kt_begin * KT, kt_end * KT);
+        return;
+    }
+    // Join the waves: sums as float4 pieces, piece d of row c at 16 d + (c ^ d % 16).
+#pragma unroll
+    for (int n = 0; n < OB; ++n) {
+        const int d = 4 * n + part;
+        *reinterpret_cast<f32x4*>(lds[wave] + (16 * d + (col ^ (d & 15))) * 16) = acc[n];
+    }
+    if (part == 0) ml[wave][col] = make_float2(m - kLift<F16>, l);
+    __syncthreads();
+    const int64_t slot0 = ((int64_t)item * a.kv_heads + hk) * R;
+    for (int u = tid; u < rows * (DP / 4); u += 64 * NS) {
+        const int row = u / (DP / 4), d = u % (DP / 4);
+        float top = ml[0][row].x;
+#pragma unroll
+        for (int w = 1; w < NS; ++w) top = fmaxf(top, ml[w][row].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NS; ++w) {
+            const float2 x = ml[w][row];
+            const float k = __builtin_amdgcn_exp2f(x.x - base);
+            sum += k * x.y;
+            o += k * *reinterpret_cast<const f32x4*>(lds[w] + (16 * d + (row ^ (d & 15))) * 16);
+        }
+        if (4 * d >= a.dim) continue;
+        if (it.parts > 1) {
+            *reinterpret_cast<f32x4*>(s.part_o + (slot0 + row) * a.dim + 4 * d) = o;
+            if (d == 0) s.part_ml[slot0 + row] = make_float2(top, sum);
+            continue;
+        }
+        const int i = (r0 + row) / a.group, h = hk * a.group + (r0 + row) - i * a.group;
+        int from, to;
+        seen_keys(a, it, i, from, to);
+        const bool empty = to <= from;
+        const float inv = empty ? 0.f : 1.f / sum;
+        const int64_t at = (int64_t)(it.start + i) * a.heads + h;
+        *reinterpret_cast<uint2*>(a.out + at * a.dim + 4 * d) =
+            make_uint2(pack_half2<F16>(o.x * inv, o.y * inv), pack_half2<F16>(o.z * inv, o.w * inv));
+        if (a.lse && d == 0) a.lse[at] = empty ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
+}
+
+// Chunks and prompts: 4 waves of 32 rows. K and V tiles go through registers into LDS one tile ahead,
+// one barrier a tile.
+constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
+template <bool F16, int DP, int KT>
+__global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_kernel(AttnArgs a, Sched s) {
+    constexpr int R = 32, ROWS = kManyRows, NT = 64 * kManyWaves;
     constexpr int CH = DP / 8;               // 16-byte pieces of a row
     constexpr int PER = KT * CH / NT;        // pieces of a tile per thread, RSTEP rows apart
     constexpr int RSTEP = NT / CH;
-    constexpr int BUF = NW > 1 ? 2 : 1;
     constexpr int TILE = KT * DP;            // elements
     constexpr int VALS = Shape<R>::kVals;    // a lane's values of a product
-    constexpr int QF = DP / Shape<R>::kDepth, SB = KT / R, PF = KT * R / 512, OB = DP / R;
+    constexpr int QF = DP / 16, SB = KT / R, OB = DP / R;
     typedef typename Shape<R>::acc acc_t;
-    __shared__ __align__(16) uint16_t lds[BUF][2][TILE];
+    __shared__ __align__(16) uint16_t lds[2][2][TILE];
 
     const int hk = blockIdx.x % a.kv_heads;
     const int item = blockIdx.x / a.kv_heads;
@@ -326,8 +664,8 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
     seen_keys(a, it, (r0 + rows - 1) / a.group, unused, hi_all);
     const int kt0 = lo_all / KT;
     const int n_all = max(0, (hi_all + KT - 1) / KT - kt0);
-    const int kt_begin = kt0 + (int)((int64_t)n_all * it.part / it.parts);
-    const int kt_end = kt0 + (int)((int64_t)n_all * (it.part + 1) / it.parts);
+    int kt_begin, kt_end;
+    part_of(it, kt0, n_all, kt_begin, kt_end);
     // the wave's tiles below sure_hi and from sure_lo on need no mask; rows that are not there
     // need none either
     int sure_lo = live ? lo : 0, sure_hi = live ? hi : 0x7fffffff, any_hi = live ? hi : 0;
@@ -340,64 +678,61 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
     sure_hi = __builtin_amdgcn_readfirstlane(sure_hi);
     any_hi = __builtin_amdgcn_readfirstlane(any_hi);
 
-    // Q^T in registers: lane holds row `col`, values kDepth c + 8 part ..
+    // Q^T in registers: lane holds row `col`, values 16 c + 8 part ..
     op8<F16> q[QF];
     {
         const uint16_t* src = a.q + (int64_t)(it.start + token) * a.q_ts + (int64_t)head * a.q_hs;
 #pragma unroll
         for (int c = 0; c < QF; ++c) {
-            const int d = Shape<R>::kDepth * c + 8 * part;
+            const int d = 16 * c + 8 * part;
             u32x4a v = {0, 0, 0, 0};
             if (live && d < a.dim) v = *reinterpret_cast<const u32x4a*>(src + d);
             q[c] = __builtin_bit_cast(op8<F16>, v);
         }
     }
 
-    // Staging: this thread's pieces are rows row0 + RSTEP i of a tile, piece `piece`. A key's offset in
-    // its page is that of the tile's first key plus the row, or the row alone where pages are no longer
-    // than tiles: (kt * KT & page_mask) + (row & page_mask), the second part fixed.
+    // Staging: this thread's pieces are rows row0 + RSTEP i of a tile, piece `piece`. The rows that a
+    // wave loads at once (2 to 8, from wave_row on) lie in one page, so the page and all but a fixed part
+    // of the address are the wave's, in scalar registers.
     const int row0 = tid / CH, piece = tid % CH;
+    const int wave_row = __builtin_amdgcn_readfirstlane(wave * (64 / CH));
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
-    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim + piece * 8;
-    const uint32_t stride = (uint32_t)a.page_stride;
+    const int last_entry = (int)min((int64_t)(max(hi_all, 1) - 1) >> a.page_shift, max(a.table_width, (int64_t)1) - 1);
+    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim;
+    const uint32_t lane_at = (uint32_t)((row0 - wave_row) * a.dim + piece * 8);
     const bool whole = a.dim == DP;
-    int page[PER];
+    int pages;  // lane i: the page of row wave_row + RSTEP i of the tile that is loaded next
     u32x4a kreg[PER], vreg[PER];
     auto load_pages = [&](int kt) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int entry = (kt * KT + row0 + RSTEP * i) >> a.page_shift;
-            // the last key's entry stands for those past it
-            page[i] = entry < a.table_width ? table[min(entry, (hi_all - 1) >> a.page_shift)] : -1;
-        }
+        const int entry = (kt * KT + wave_row + RSTEP * min(lane, PER - 1)) >> a.page_shift;
+        pages = entry < a.table_width ? table[min(entry, last_entry)] : -1;
     };
     auto load_tile = [&](int kt) {
-        const int64_t tile_at = head_at + (int64_t)((kt * KT) & page_mask) * a.dim;
-        bool good = whole;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) good &= (uint32_t)page[i] < (uint64_t)a.pages;
-        if (kt * KT >= lo_all && (kt + 1) * KT <= hi_all && __all(good)) {
+        const bool good = __all((uint32_t)pages < (uint64_t)a.pages);
+        if (whole && good && kt * KT >= lo_all && (kt + 1) * KT <= hi_all) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + tile_at +
-                                    (uint32_t)(((row0 + RSTEP * i) & page_mask) * a.dim);
-                kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at);
-                vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at);
+                const uint32_t page = (uint32_t)lane_value(pages, i);
+                const int64_t at = (int64_t)((uint64_t)page * (uint32_t)a.page_stride) + head_at +
+                                   (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * DP;
+                kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
+                vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
             }
             return;
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int row = row0 + RSTEP * i, key = kt * KT + row;
+            const uint32_t page = (uint32_t)lane_value(pages, i);
+            const int key = kt * KT + row0 + RSTEP * i;
             u32x4a kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
             if (key >= lo_all && key < hi_all) {
-                if ((uint32_t)page[i] < (uint64_t)a.pages) {
+                if (page < (uint64_t)a.pages) {
                     if (piece * 8 < a.dim) {
-                        const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + tile_at +
-                                            (uint32_t)((row & page_mask) * a.dim);
-                        kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at);
-                        vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at);
+                        const int64_t at = (int64_t)((uint64_t)page * (uint32_t)a.page_stride) + head_at +
+                                           (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * a.dim;
+                        kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
+                        vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
                     }
                 } else {  // outside the pool: NaN scores, so the rows that see the key are NaN
                     kv = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
@@ -414,12 +749,12 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
 #pragma unroll
         for (int i = 0; i < VALS; ++i) acc[n][i] = 0.f;
     float m = -INFINITY, l = 0.f;
-    bool redo = false;
+    bool again = false;
     const float factor = a.scale * kLog2e;
 
-    // A lane's reads of V: rows 32 f' + kRow e + v_row, pieces (R / 8) n + v_piece, from value v_sub on.
+    // a lane's transposing reads: rows v_row + 16 f and + 8, pieces 4 n + v_piece, from value v_sub on
     const int v_row = 4 * part + ((lane & 15) >> 2);
-    const int v_piece = (R == 32 ? 2 * ((lane >> 4) & 1) : 0) + ((lane & 3) >> 1);
+    const int v_piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     const int v_sub = 4 * (lane & 1);
 
     if (kt_begin < kt_end) {
@@ -428,8 +763,8 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
         load_pages(kt_begin + 1);
     }
     for (int kt = kt_begin; kt < kt_end; ++kt) {
-        uint16_t* kl = lds[BUF > 1 ? kt & 1 : 0][0];
-        uint16_t* vl = lds[BUF > 1 ? kt & 1 : 0][1];
+        uint16_t* kl = lds[kt & 1][0];
+        uint16_t* vl = lds[kt & 1][1];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int row = row0 + RSTEP * i;
@@ -441,107 +776,46 @@ __global__ __launch_bounds__(64 * NW, DP > 128 ? 1 : 2) void attn_kernel(AttnArg
             load_pages(kt + 2);
         }
         // two buffers: the other one's readers are past the previous barrier
-        if (NW > 1) __syncthreads();
+        __syncthreads();
         const int key0 = kt * KT;
         if (key0 >= any_hi) continue;  // keys past every row of this wave
 
         acc_t sc[SB];
 #pragma unroll
-        for (int kb = 0; kb < SB; ++kb) {
+        for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
             for (int i = 0; i < VALS; ++i) sc[kb][i] = 0.f;
+        // blocks of keys inside: their products do not wait for each other
 #pragma unroll
-            for (int c = 0; c < QF; ++c) {
+        for (int c = 0; c < QF; ++c)
+#pragma unroll
+            for (int kb = 0; kb < SB; ++kb) {
                 const int row = kb * R + col;
                 const op8<F16> kf = *reinterpret_cast<const op8<F16>*>(
-                    kl + row * DP + ((((Shape<R>::kDepth / 8) * c + part) ^ swizzle_k<DP>(row)) * 8));
+                    kl + row * DP + (((2 * c + part) ^ swizzle_k<DP>(row)) * 8));
                 sc[kb] = product<F16>(kf, q[c], sc[kb]);
             }
-        }
-        if (key0 < sure_lo || key0 + KT > sure_hi) {
+        if (key0 < sure_lo || key0 + KT > sure_hi) mask_scores<R>(sc, key0, part, lo, hi);
+        softmax_tile<F16, R>(sc, acc, factor, m, l);
+        op8<F16> p[2 * SB];
 #pragma unroll
-            for (int kb = 0; kb < SB; ++kb)
+        for (int f = 0; f < 2 * SB; ++f)
+            p[f] = f % 2 ? pack8<F16>(__builtin_shufflevector(sc[f / 2], sc[f / 2], 8, 9, 10, 11),
+                                      __builtin_shufflevector(sc[f / 2], sc[f / 2], 12, 13, 14, 15))
+                         : pack8<F16>(__builtin_shufflevector(sc[f / 2], sc[f / 2], 0, 1, 2, 3),
+                                      __builtin_shufflevector(sc[f / 2], sc[f / 2], 4, 5, 6, 7));
+        if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) again |= tile_not_finite<F16, TILE / 8>(vl);
 #pragma unroll
-                for (int i = 0; i < VALS; ++i) {
-                    const int key = key0 + kb * R + (i >> 2) * 8 + 4 * part + (i & 3);
-                    if (key < lo || key >= hi) sc[kb][i] = -INFINITY;
-                }
-        }
-        float top = sc[0][0];
+        for (int f = 0; f < 2 * SB; ++f)
 #pragma unroll
-        for (int kb = 0; kb < SB; ++kb)
-#pragma unroll
-            for (int i = 0; i < VALS; ++i) top = fmaxf(top, sc[kb][i]);
-        top = max_of_row<R>(top) * factor;
-        if (__any(top > m + kSlack)) {
-            const float m_new = fmaxf(m, top);
-            const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
-            l *= keep;
-#pragma unroll
-            for (int n = 0; n < OB; ++n)
-#pragma unroll
-                for (int i = 0; i < VALS; ++i) acc[n][i] *= keep;
-            m = m_new;
-        }
-        const float base = m == -INFINITY ? 0.f : m - kLift<F16>;
-#pragma unroll
-        for (int kb = 0; kb < SB; ++kb)
-#pragma unroll
-            for (int i = 0; i < VALS; ++i) {
-                sc[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[kb][i], factor, -base));
-                l += sc[kb][i];
+            for (int n = 0; n < OB; ++n) {
+                uint16_t* src = vl + (v_row + 16 * f) * DP + ((v_piece + 4 * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
+                acc[n] = product<F16>(read_column<F16>(src, src + 8 * DP), p[f], acc[n]);
             }
-        // rounded to 16 bits for the product with V; their sum l is taken before the rounding
-        op8<F16> p[PF];
-#pragma unroll
-        for (int f = 0; f < PF; ++f) {
-            float x[8];  // of one block of scores (two to a block), or of two blocks (R = 16)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = R == 32 ? sc[f / 2][8 * (f % 2) + i] : sc[2 * f + i / 4][i % 4];
-            p[f] = __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(x[0], x[1]), pack_half2<F16>(x[2], x[3]),
-                                                       pack_half2<F16>(x[4], x[5]), pack_half2<F16>(x[6], x[7])});
-        }
-        // A weight of zero times an infinite or NaN value is NaN: where the tile holds keys that some
-        // row does not see, look for such values.
-        if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) {
-#pragma unroll 1
-            for (int x = lane; x < TILE / 8; x += 64) {
-                const u32x4a w = *reinterpret_cast<const u32x4a*>(vl + x * 8);
-                redo |= not_finite2<F16>(w.x) || not_finite2<F16>(w.y) || not_finite2<F16>(w.z) || not_finite2<F16>(w.w);
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < OB; ++n) {
-            const int at = ((v_piece + (R / 8) * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
-#pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                uint16_t* src = vl + (v_row + (R == 32 ? 16 : 32) * f) * DP + at;
-                const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)src);
-                const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(src + (R == 32 ? 8 : 16) * DP));
-                const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
-                acc[n] = product<F16>(__builtin_bit_cast(op8<F16>, u32x4a{w0.x, w0.y, w1.x, w1.y}), p[f], acc[n]);
-            }
-        }
     }
 
-    if (__any(redo)) {  // this wave's rows again, one by one, each over the keys that it sees alone
-#pragma unroll 1
-        for (int x = wave * R; x < min(wave * R + R, rows); ++x) {
-            const int i = (r0 + x) / a.group, h = hk * a.group + (r0 + x) - i * a.group;
-            int from, to;
-            seen_keys(a, it, i, from, to);
-            float mx, lx, o[4];
-            scalar_row<F16>(a, it.b, it.start + i, h, max(from, kt_begin * KT), min(to, kt_end * KT), mx, lx, o);
-            if (it.parts == 1) {
-                store_scalar_row<F16>(a, it.start + i, h, to <= from, mx, lx, o);
-                continue;
-            }
-            const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + x;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if (lane + 64 * y < a.dim) s.part_o[slot * a.dim + lane + 64 * y] = o[y];
-            if (lane == 0) s.part_ml[slot] = make_float2(mx, lx);
-        }
+    if (__any(again)) {  // this wave's rows
+        take_rows_again<F16, ROWS>(a, s, it, item, hk, wave * R, min(wave * R + R, rows), 1, kt_begin * KT, kt_end * KT);
         return;
     }
     l = sum_of_row<R>(l);
@@ -651,33 +925,39 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
     }
 }
 
-// How a call runs: the few-rows kernel (16-row tiles), the many-rows kernel (tiles of kManyRows) or
-// both, and whether their tiles are cut along the keys.
-constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
+// How a call runs: the few-rows kernel, the many-rows kernel or both, and whether their tiles are cut
+// along the keys.
 constexpr int kFewMax = 32;  // requests of more rows are the many-rows kernel's
-constexpr int kFewPart = 2, kManyPart = 8;
 
 struct Launches {
     struct One {
         int64_t tiles = 0;  // at most so many tiles (0: not launched)
         int rows = 0, rows_lo = 0, rows_hi = 0;
-        int parts = 0;
-        int64_t items() const { return tiles + parts; }
-        size_t slots(int64_t kv_heads) const { return parts ? (size_t)(items() * kv_heads * rows) : 0; }
+        int parts = 0, min_part = 1;
+        int64_t items = 0;
+        size_t slots(int64_t kv_heads) const { return parts ? (size_t)(items * kv_heads * rows) : 0; }
+        // Cut into about `want` parts of at least `least` tiles of `tile` keys.
+        void cut(int64_t want, int least, int64_t table_keys, int tile) {
+            min_part = least;
+            const int64_t most = (table_keys + (int64_t)tile * least - 1) / ((int64_t)tile * least);  // parts of a tile
+            if (tiles && most > 1 && want > 0) parts = (int)want;
+            items = parts ? (tiles + parts < tiles * most ? tiles + parts : tiles * most) : tiles;
+        }
     } few, many;
+    int few_waves = 4;
 };
 
-Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t table_keys, int64_t requests,
-                       int64_t max_new) {
+Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
+                       int64_t requests, int64_t max_new) {
     Launches p;
     const int64_t group = heads / kv_heads, rows = tokens * group, cus = device_cu_count();
     const int64_t holders = requests + 1 < tokens ? requests + 1 : tokens;  // requests with rows
     if (max_new <= kFewMax / group || rows <= kFewMax) {
-        p.few.tiles = holders + rows / 16;
+        p.few.tiles = holders + rows / kFewRows;
         p.few.rows_hi = 0x7fffffff;
     } else {
         if (requests > 1) {
-            p.few.tiles = 2 * holders;
+            p.few.tiles = kFewMax / kFewRows * holders;
             p.few.rows_hi = kFewMax;
             p.many.rows_lo = kFewMax;
         }
@@ -685,35 +965,44 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
         p.many.tiles = rows / kManyRows + (holders < large ? holders : large);
         p.many.rows_hi = 0x7fffffff;
     }
-    p.few.rows = 16;
+    p.few.rows = kFewRows;
     p.many.rows = kManyRows;
-    // Cut where whole tiles would leave workgroup slots empty: 8 waves of the few-rows kernel fit a
-    // CU, 2 workgroups of the other. Twice as many parts, so that uneven ends are short.
-    if (p.few.tiles && table_keys > 32 * kFewPart) p.few.parts = (int)((cus * 16 + kv_heads - 1) / kv_heads);
+    // Few rows. Up to 1024 keys one workgroup of 8 waves takes them all, and there is nothing to join;
+    // beyond, 4 waves a workgroup and twice as many parts as workgroups fit the chip, so that uneven
+    // ends are short.
+    if (table_keys <= 1024) p.few_waves = 8;
+    p.few.cut(p.few_waves == 8 ? 0 : (cus * 4 + kv_heads - 1) / kv_heads, 4, table_keys, 32);
+    // Many rows: cut only where whole tiles would leave workgroup slots (2 a CU) empty.
     const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
-    if (p.many.tiles && p.many.tiles < slots && table_keys > 64 * kManyPart) p.many.parts = (int)(2 * slots);
+    const int tile = head_dim > 128 ? 32 : 64;
+    p.many.cut(p.many.tiles < slots ? 2 * slots : 0, 512 / tile, table_keys, tile);
     return p;
 }
 
 template <bool F16, int DP>
 hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream) {
     constexpr int KT = DP > 128 ? 32 : 64;
+    constexpr int RP = 1024 / DP;
     const size_t few_slots = p.few.slots(a.kv_heads), many_slots = p.many.slots(a.kv_heads);
     float* o = a.partial;
     float2* ml = reinterpret_cast<float2*>(o + (few_slots + many_slots) * a.dim);
-    const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, kFewPart, o, ml};
-    const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, kManyPart * 64 / KT, o + few_slots * a.dim,
-                     ml + few_slots};
+    const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, p.few.min_part, o, ml};
+    const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, p.many.min_part, o + few_slots * a.dim, ml + few_slots};
     if (p.many.tiles)
-        attn_kernel<F16, DP, 32, kManyWaves, KT>
-            <<<(unsigned)(p.many.items() * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
-    if (p.few.tiles) attn_kernel<F16, DP, 16, 1, 32><<<(unsigned)(p.few.items() * a.kv_heads), 64, 0, stream>>>(a, few);
+        attn_many_kernel<F16, DP, KT><<<(unsigned)(p.many.items * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
+    if (p.few.tiles) {
+        const unsigned grid = (unsigned)(p.few.items * a.kv_heads);
+        // (heads above 128 need more registers than 8 waves a workgroup can have)
+        constexpr int kWide = DP > 128 ? 4 : 8;
+        if (p.few_waves == 8) attn_few_kernel<F16, DP, kWide><<<grid, 64 * kWide, 0, stream>>>(a, few);
+        else attn_few_kernel<F16, DP, 4><<<grid, 256, 0, stream>>>(a, few);
+    }
     if (p.many.parts)
-        join_kernel<F16, DP, kManyRows, KT, 1024 / DP>
-            <<<dim3((unsigned)(p.many.tiles * a.kv_heads), kManyRows / (1024 / DP)), 256, 0, stream>>>(a, many);
+        join_kernel<F16, DP, kManyRows, KT, RP>
+            <<<dim3((unsigned)(p.many.tiles * a.kv_heads), kManyRows / RP), 256, 0, stream>>>(a, many);
     if (p.few.parts)
-        join_kernel<F16, DP, 16, 32, 1>
-            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < 16 ? a.group : 16), 256, 0, stream>>>(a, few);
+        join_kernel<F16, DP, kFewRows, 32, 1>
+            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < kFewRows ? a.group : kFewRows), 256, 0, stream>>>(a, few);
     return hipGetLastError();
 }
 
@@ -723,7 +1012,7 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 size_t paged_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
                                  int64_t requests, int64_t max_new) {
-    const Launches p = plan_launches(tokens, heads, kv_heads, table_keys, requests, max_new);
+    const Launches p = plan_launches(tokens, heads, kv_heads, head_dim, table_keys, requests, max_new);
     return (p.few.slots(kv_heads) + p.many.slots(kv_heads)) * (size_t)(4 * head_dim + 8);
 }
 
@@ -738,7 +1027,7 @@ hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, 
         else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.table_width << a.page_shift, a.requests, max_new);
+    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_keys, a.requests, max_new);
     if (a.dim <= 64) return f16 ? launch_tiles<true, 64>(a, p, stream) : launch_tiles<false, 64>(a, p, stream);
     if (a.dim <= 128) return f16 ? launch_tiles<true, 128>(a, p, stream) : launch_tiles<false, 128>(a, p, stream);
     return f16 ? launch_tiles<true, 256>(a, p, stream) : launch_tiles<false, 256>(a, p, stream);

@@ -351,6 +351,19 @@ def test_attention_pages_outside_the_pool(dim):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dim", [64, 20])
+def test_attention_lengths_past_the_table(dim):
+    # lengths that no table holds: NaN rows, and no time spent on keys that are not there
+    c = Case([(100, 1), (60, 60), (90, 1), (64, 40)], 4, 2, dim, 16, BF)
+    whole = c.run()[0].cpu()
+    c.kv[0], c.kv[1] = 2**31 - 1, 2**31 - 1
+    for kw in (dict(), dict(window=8), dict(max_new=60), dict(causal=False)):
+        out, lse = (x.cpu() for x in c.run(**kw))
+        assert out[:61].isnan().all() and lse[:61].isnan().all()
+        assert out[61:].isfinite().all() and lse[61:].isfinite().all()
+    assert torch.equal(c.run()[0].cpu()[61:], whole[61:])
+
+
 @pytest.mark.parametrize("dim", [128, 64, 24])
 def test_attention_strides_and_alignment(dim):
     c = Case(CHUNKS, 4, 2, dim, 16, BF)

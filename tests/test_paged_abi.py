@@ -111,6 +111,7 @@ def test_attention_unsupported_and_no_ops(lib):
     assert attention(lib, requests=65537) == UNSUPPORTED
     assert attention(lib, tokens=2**29) == UNSUPPORTED
     assert attention(lib, width=2**27) == UNSUPPORTED
+    assert attention(lib, width=2**26) == UNSUPPORTED
     assert attention(lib, pages=2**31) == UNSUPPORTED
     assert attention(lib, tokens=0, q=None, out=None) == OK
     assert attention(lib, heads=0, kv_heads=0, q=None, out=None) == OK
