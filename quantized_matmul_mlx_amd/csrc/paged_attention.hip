@@ -434,7 +434,7 @@ __device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& i
 // addresses. A tile's keys are used before its values: their registers take the next tile's loads
 // at once, so a wave has about a tile (16 KB at 128 values) in flight all the time.
 constexpr int kFewRows = 16;
-template <bool F16, int DP, int NS>
+template <bool F16, int DP, int NS, bool FULL>
 __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(AttnArgs a, Sched s) {
     constexpr int KT = 32, R = 16;
     constexpr int QF = DP / 32, OB = DP / 16;
@@ -442,6 +442,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
     __shared__ __align__(16) uint8_t lds[NS][BYTES];
     __shared__ float2 ml[NS][R];
 
+    const int dim = FULL ? DP : a.dim;  // FULL: the head size is DP
     const int hk = blockIdx.x % a.kv_heads;
     const int item = blockIdx.x / a.kv_heads;
     Item it;
@@ -470,52 +471,58 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
-    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim + part * 8;
-    const uint32_t stride = (uint32_t)a.page_stride;
-    const bool whole = a.dim == DP;
-    int page[2];
+    const int64_t head_at = ((int64_t)hk << a.page_shift) * dim;
+    const int last_entry = min(hi_all - 1, a.table_keys - 1) >> a.page_shift;
+    // Loads need no condition: keys before lo_all and from hi_all on lie in pages that the item's keys
+    // have, a page outside the pool is replaced by page 0, pieces past the head size by piece 0. What
+    // such a load brings is put right before its use (fix).
+    int page[2], bad = 0;
     u32x4a kreg[2][QF], vreg[2][QF];
     auto load_pages = [&](int kt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int entry = (kt * KT + 16 * i + col) >> a.page_shift;
-            // the last key's entry stands for those past it
-            page[i] = entry < a.table_width ? table[min(entry, (hi_all - 1) >> a.page_shift)] : -1;
+            page[i] = table[min(entry, last_entry)];
+            if ((int64_t)min(kt * KT + 16 * i + col, hi_all - 1) >= a.table_keys) page[i] = -1;
         }
     };
     auto load_tile = [&](int kt) {
-        const bool good = (uint32_t)page[0] < (uint64_t)a.pages && (uint32_t)page[1] < (uint64_t)a.pages;
-        if (whole && kt * KT >= lo_all && (kt + 1) * KT <= hi_all && __all(good)) {
-            uint64_t at[2];
+        bad = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                at[i] = (uint64_t)(uint32_t)page[i] * stride + head_at + (uint32_t)(((kt * KT + 16 * i + col) & page_mask) * DP);
+        for (int i = 0; i < 2; ++i) {
+            const bool ok = (uint32_t)page[i] < (uint64_t)a.pages;
+            if (!ok) bad |= 1 << i;
+            const uint64_t at = (uint64_t)(uint32_t)(ok ? page[i] : 0) * (uint32_t)a.page_stride + head_at +
+                                (uint32_t)(((kt * KT + 16 * i + col) & page_mask) * dim);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < QF; ++c) kreg[i][c] = *reinterpret_cast<const u32x4a*>(a.k_cache + at[i] + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < QF; ++c) vreg[i][c] = *reinterpret_cast<const u32x4a*>(a.v_cache + at[i] + 32 * c);
-            return;
+            for (int c = 0; c < QF; ++c) {
+                const int d = 32 * c + 8 * part;
+                kreg[i][c] = *reinterpret_cast<const u32x4a*>(a.k_cache + at + (d < dim ? d : 0));
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int key = kt * KT + 16 * i + col;
-            const bool in = key >= lo_all && key < hi_all, ok = (uint32_t)page[i] < (uint64_t)a.pages;
-            const uint64_t at = (uint64_t)(uint32_t)page[i] * stride + head_at + (uint32_t)((key & page_mask) * a.dim);
-            // outside the pool: NaN scores, so the rows that see the key are NaN
-            const uint32_t none = in && !ok ? 0x7FFF7FFFu : 0u;
+            const uint64_t at = (uint64_t)(uint32_t)(bad >> i & 1 ? 0 : page[i]) * (uint32_t)a.page_stride + head_at +
+                                (uint32_t)(((kt * KT + 16 * i + col) & page_mask) * dim);
 #pragma unroll
             for (int c = 0; c < QF; ++c) {
-                u32x4a kv = {none, none, none, none}, vv = {0, 0, 0, 0};
-                if (in && ok && 32 * c + 8 * part < a.dim) {
-                    kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at + 32 * c);
-                    vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at + 32 * c);
-                }
-                kreg[i][c] = kv;
-                vreg[i][c] = vv;
+                const int d = 32 * c + 8 * part;
+                vreg[i][c] = *reinterpret_cast<const u32x4a*>(a.v_cache + at + (d < dim ? d : 0));
+            }
+        }
+    };
+    auto fix_tile = [&](int kt) {
+        asm volatile("");  // keeps the caller's branch
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = kt * KT + 16 * i + col;
+            const bool in = key >= lo_all && key < hi_all, out_of_pool = bad >> i & 1;
+#pragma unroll
+            for (int c = 0; c < QF; ++c) {
+                // NaN scores where the page is outside the pool: the rows that see the key are NaN
+                if (out_of_pool) kreg[i][c] = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
+                else if (32 * c + 8 * part >= dim) kreg[i][c] = u32x4a{0, 0, 0, 0};
+                if (!in || out_of_pool) vreg[i][c] = u32x4a{0, 0, 0, 0};
             }
         }
     };
@@ -533,7 +540,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 #pragma unroll
         for (int c = 0; c < QF; ++c) {
             u32x4a v = {0, 0, 0, 0};
-            if (live && 32 * c + 8 * part < a.dim) v = *reinterpret_cast<const u32x4a*>(src + 32 * c + 8 * part);
+            if (live && 32 * c + 8 * part < dim) v = *reinterpret_cast<const u32x4a*>(src + 32 * c + 8 * part);
             q[c] = __builtin_bit_cast(op8<F16>, v);
         }
     }
@@ -548,6 +555,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
     const int v_row = 4 * part + (col >> 2), v_piece = (lane & 3) >> 1, v_sub = 4 * (lane & 1);
 
     for (; kt < kt_end; kt += NS) {
+        if (dim < DP || kt * KT < lo_all || (kt + 1) * KT > hi_all || __any(bad)) fix_tile(kt);
         f32x4 sc[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -571,13 +579,17 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
             mask_scores<R>(sc, key0, part, lo, hi);
             if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) again |= tile_not_finite<F16, KT * DP / 8>(vl);
         }
-        softmax_tile<F16, R>(sc, acc, factor, m, l);
-        const op8<F16> p = pack8<F16>(sc[0], sc[1]);
+        op8<F16> vf[OB];  // all of them asked for before the softmax, whose time hides theirs
 #pragma unroll
         for (int n = 0; n < OB; ++n) {
             uint16_t* src = vl + v_row * DP + ((v_piece + 2 * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
-            acc[n] = product<F16>(read_column<F16>(src, src + 16 * DP), p, acc[n]);
+            vf[n] = read_column<F16>(src, src + 16 * DP);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        softmax_tile<F16, R>(sc, acc, factor, m, l);
+        const op8<F16> p = pack8<F16>(sc[0], sc[1]);
+#pragma unroll
+        for (int n = 0; n < OB; ++n) acc[n] = product<F16>(vf[n], p, acc[n]);
     }
 
     l = sum_of_row<R>(l);
@@ -609,9 +621,9 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
             sum += k * x.y;
             o += k * *reinterpret_cast<const f32x4*>(lds[w] + (16 * d + (row ^ (d & 15))) * 16);
         }
-        if (4 * d >= a.dim) continue;
+        if (4 * d >= dim) continue;
         if (it.parts > 1) {
-            *reinterpret_cast<f32x4*>(s.part_o + (slot0 + row) * a.dim + 4 * d) = o;
+            *reinterpret_cast<f32x4*>(s.part_o + (slot0 + row) * dim + 4 * d) = o;
             if (d == 0) s.part_ml[slot0 + row] = make_float2(top, sum);
             continue;
         }
@@ -621,7 +633,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
         const bool empty = to <= from;
         const float inv = empty ? 0.f : 1.f / sum;
         const int64_t at = (int64_t)(it.start + i) * a.heads + h;
-        *reinterpret_cast<uint2*>(a.out + at * a.dim + 4 * d) =
+        *reinterpret_cast<uint2*>(a.out + at * dim + 4 * d) =
             make_uint2(pack_half2<F16>(o.x * inv, o.y * inv), pack_half2<F16>(o.z * inv, o.w * inv));
         if (a.lse && d == 0) a.lse[at] = empty ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
@@ -630,7 +642,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 // Chunks and prompts: 4 waves of 32 rows. K and V tiles go through registers into LDS one tile ahead,
 // one barrier a tile.
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
-template <bool F16, int DP, int KT>
+template <bool F16, int DP, int KT, bool FULL>
 __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_kernel(AttnArgs a, Sched s) {
     constexpr int R = 32, ROWS = kManyRows, NT = 64 * kManyWaves;
     constexpr int CH = DP / 8;               // 16-byte pieces of a row
@@ -642,6 +654,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     typedef typename Shape<R>::acc acc_t;
     __shared__ __align__(16) uint16_t lds[2][2][TILE];
 
+    const int dim = FULL ? DP : a.dim;
     const int hk = blockIdx.x % a.kv_heads;
     const int item = blockIdx.x / a.kv_heads;
     Item it;
@@ -686,7 +699,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
         for (int c = 0; c < QF; ++c) {
             const int d = 16 * c + 8 * part;
             u32x4a v = {0, 0, 0, 0};
-            if (live && d < a.dim) v = *reinterpret_cast<const u32x4a*>(src + d);
+            if (live && d < dim) v = *reinterpret_cast<const u32x4a*>(src + d);
             q[c] = __builtin_bit_cast(op8<F16>, v);
         }
     }
@@ -698,48 +711,41 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     const int wave_row = __builtin_amdgcn_readfirstlane(wave * (64 / CH));
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
-    const int last_entry = (int)min((int64_t)(max(hi_all, 1) - 1) >> a.page_shift, max(a.table_width, (int64_t)1) - 1);
-    const int64_t head_at = ((int64_t)hk << a.page_shift) * a.dim;
-    const uint32_t lane_at = (uint32_t)((row0 - wave_row) * a.dim + piece * 8);
-    const bool whole = a.dim == DP;
-    int pages;  // lane i: the page of row wave_row + RSTEP i of the tile that is loaded next
+    const int last_entry = min(max(hi_all, 1) - 1, a.table_keys - 1) >> a.page_shift;
+    const int64_t head_at = ((int64_t)hk << a.page_shift) * dim;
+    const uint32_t lane_at = (uint32_t)((row0 - wave_row) * dim + (piece * 8 < dim ? piece * 8 : 0));
+    // As in the other kernel, loads need no condition and are put right before their use. Lane i of
+    // `pages` holds the page of row wave_row + RSTEP i of the tile that is loaded next.
+    int pages;
+    uint32_t bad = 0;
     u32x4a kreg[PER], vreg[PER];
     auto load_pages = [&](int kt) {
-        const int entry = (kt * KT + wave_row + RSTEP * min(lane, PER - 1)) >> a.page_shift;
-        pages = entry < a.table_width ? table[min(entry, last_entry)] : -1;
+        const int key = kt * KT + wave_row + RSTEP * min(lane, PER - 1);
+        pages = table[min(key >> a.page_shift, last_entry)];
+        if (min(key, hi_all - 1) >= a.table_keys) pages = -1;
     };
     auto load_tile = [&](int kt) {
-        const bool good = __all((uint32_t)pages < (uint64_t)a.pages);
-        if (whole && good && kt * KT >= lo_all && (kt + 1) * KT <= hi_all) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t page = (uint32_t)lane_value(pages, i);
-                const int64_t at = (int64_t)((uint64_t)page * (uint32_t)a.page_stride) + head_at +
-                                   (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * DP;
-                kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
-                vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
-            }
-            return;
-        }
+        const bool ok = (uint32_t)pages < (uint64_t)a.pages;
+        bad = (uint32_t)__ballot(!ok);
+        const int page = ok ? pages : 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t page = (uint32_t)lane_value(pages, i);
+            const int64_t at = (int64_t)((uint64_t)(uint32_t)lane_value(page, i) * (uint32_t)a.page_stride) + head_at +
+                               (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * dim;
+            kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
+            vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
+        }
+    };
+    auto fix_tile = [&](int kt) {
+        asm volatile("");  // keeps the caller's branch
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
             const int key = kt * KT + row0 + RSTEP * i;
-            u32x4a kv = {0, 0, 0, 0}, vv = {0, 0, 0, 0};
-            if (key >= lo_all && key < hi_all) {
-                if (page < (uint64_t)a.pages) {
-                    if (piece * 8 < a.dim) {
-                        const int64_t at = (int64_t)((uint64_t)page * (uint32_t)a.page_stride) + head_at +
-                                           (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * a.dim;
-                        kv = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
-                        vv = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
-                    }
-                } else {  // outside the pool: NaN scores, so the rows that see the key are NaN
-                    kv = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
-                }
-            }
-            kreg[i] = kv;
-            vreg[i] = vv;
+            const bool in = key >= lo_all && key < hi_all, out_of_pool = bad >> i & 1;
+            // NaN scores where the page is outside the pool: the rows that see the key are NaN
+            if (out_of_pool) kreg[i] = u32x4a{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu};
+            else if (piece * 8 >= dim) kreg[i] = u32x4a{0, 0, 0, 0};
+            if (!in || out_of_pool) vreg[i] = u32x4a{0, 0, 0, 0};
         }
     };
 
@@ -763,6 +769,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
         load_pages(kt_begin + 1);
     }
     for (int kt = kt_begin; kt < kt_end; ++kt) {
+        if (dim < DP || kt * KT < lo_all || (kt + 1) * KT > hi_all || bad) fix_tile(kt);
         uint16_t* kl = lds[kt & 1][0];
         uint16_t* vl = lds[kt & 1][1];
 #pragma unroll
@@ -823,13 +830,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     const float m_out = m - kLift<F16>;
     if (it.parts > 1) {
         const int64_t slot = ((int64_t)item * a.kv_heads + hk) * ROWS + r;
-        float* o = s.part_o + slot * a.dim;
+        float* o = s.part_o + slot * dim;
 #pragma unroll
         for (int n = 0; n < OB; ++n)
 #pragma unroll
             for (int i = 0; i < VALS / 4; ++i) {
                 const int d = R * n + 8 * i + 4 * part;
-                if (d < a.dim)
+                if (d < dim)
                     *reinterpret_cast<f32x4*>(o + d) =
                         f32x4{acc[n][4 * i], acc[n][4 * i + 1], acc[n][4 * i + 2], acc[n][4 * i + 3]};
             }
@@ -839,13 +846,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     const bool empty = hi <= lo;
     const float inv = empty ? 0.f : 1.f / l;
     const int64_t row = (int64_t)(it.start + token) * a.heads + head;
-    uint16_t* o = a.out + row * a.dim;
+    uint16_t* o = a.out + row * dim;
 #pragma unroll
     for (int n = 0; n < OB; ++n)
 #pragma unroll
         for (int i = 0; i < VALS / 4; ++i) {
             const int d = R * n + 8 * i + 4 * part;
-            if (d < a.dim)
+            if (d < dim)
                 *reinterpret_cast<uint2*>(o + d) = make_uint2(pack_half2<F16>(acc[n][4 * i] * inv, acc[n][4 * i + 1] * inv),
                                                               pack_half2<F16>(acc[n][4 * i + 2] * inv, acc[n][4 * i + 3] * inv));
         }
@@ -979,7 +986,7 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     return p;
 }
 
-template <bool F16, int DP>
+template <bool F16, int DP, bool FULL>
 hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream) {
     constexpr int KT = DP > 128 ? 32 : 64;
     constexpr int RP = 1024 / DP;
@@ -989,13 +996,13 @@ hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream
     const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, p.few.min_part, o, ml};
     const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, p.many.min_part, o + few_slots * a.dim, ml + few_slots};
     if (p.many.tiles)
-        attn_many_kernel<F16, DP, KT><<<(unsigned)(p.many.items * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
+        attn_many_kernel<F16, DP, KT, FULL><<<(unsigned)(p.many.items * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
     if (p.few.tiles) {
         const unsigned grid = (unsigned)(p.few.items * a.kv_heads);
         // (heads above 128 need more registers than 8 waves a workgroup can have)
         constexpr int kWide = DP > 128 ? 4 : 8;
-        if (p.few_waves == 8) attn_few_kernel<F16, DP, kWide><<<grid, 64 * kWide, 0, stream>>>(a, few);
-        else attn_few_kernel<F16, DP, 4><<<grid, 256, 0, stream>>>(a, few);
+        if (p.few_waves == 8) attn_few_kernel<F16, DP, kWide, FULL><<<grid, 64 * kWide, 0, stream>>>(a, few);
+        else attn_few_kernel<F16, DP, 4, FULL><<<grid, 256, 0, stream>>>(a, few);
     }
     if (p.many.parts)
         join_kernel<F16, DP, kManyRows, KT, RP>
@@ -1004,6 +1011,11 @@ hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream
         join_kernel<F16, DP, kFewRows, 32, 1>
             <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < kFewRows ? a.group : kFewRows), 256, 0, stream>>>(a, few);
     return hipGetLastError();
+}
+
+template <bool F16, int DP>
+hipError_t launch_dim(const AttnArgs& a, const Launches& p, hipStream_t stream) {
+    return a.dim == DP ? launch_tiles<F16, DP, true>(a, p, stream) : launch_tiles<F16, DP, false>(a, p, stream);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -1017,9 +1029,10 @@ size_t paged_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, hipStream_t stream) {
-    // 16-byte loads of every row, and heads of whole 16-byte pieces (pages apart by a 32-bit count)
+    // 16-byte loads of every row, and heads of whole 16-byte pieces (pages apart by a 32-bit count;
+    // without any page there is nothing that a load could be pointed at instead)
     const bool pieces = a.dim % 8 == 0 && a.q_ts % 8 == 0 && a.q_hs % 8 == 0 && a.page_stride % 8 == 0 &&
-                        a.page_stride < (1LL << 32) &&
+                        a.page_stride < (1LL << 32) && a.pages > 0 && a.table_keys > 0 &&
                         aligned16(a.q) && aligned16(a.k_cache) && aligned16(a.v_cache) && aligned16(a.out);
     if (!pieces) {
         const unsigned grid = (unsigned)a.tokens * (unsigned)a.heads;
@@ -1028,9 +1041,9 @@ hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, 
         return hipGetLastError();
     }
     const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_keys, a.requests, max_new);
-    if (a.dim <= 64) return f16 ? launch_tiles<true, 64>(a, p, stream) : launch_tiles<false, 64>(a, p, stream);
-    if (a.dim <= 128) return f16 ? launch_tiles<true, 128>(a, p, stream) : launch_tiles<false, 128>(a, p, stream);
-    return f16 ? launch_tiles<true, 256>(a, p, stream) : launch_tiles<false, 256>(a, p, stream);
+    if (a.dim <= 64) return f16 ? launch_dim<true, 64>(a, p, stream) : launch_dim<false, 64>(a, p, stream);
+    if (a.dim <= 128) return f16 ? launch_dim<true, 128>(a, p, stream) : launch_dim<false, 128>(a, p, stream);
+    return f16 ? launch_dim<true, 256>(a, p, stream) : launch_dim<false, 256>(a, p, stream);
 }
 
 }  // namespace qaff

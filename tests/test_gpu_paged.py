@@ -351,6 +351,39 @@ def test_attention_pages_outside_the_pool(dim):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dim", [64, 96, 20])
+@pytest.mark.parametrize("stale", [-1, 10**6])
+def test_attention_windows_over_released_pages(dim, stale):
+    # the pages that every window has left behind are given back: their entries are stale
+    c = Case([(700, 1), (300, 5), (640, 80)], 4, 2, dim, 8, HF)
+    for b in range(3):
+        first = c.kv[b] - c.new[b] - 100 + 1          # the first key that the request's first token sees
+        c.tables[b, :first // 8] = stale
+    c.check(c.run(window=100, max_new=80), window=100)
+
+
+@pytest.mark.parametrize("dim", [8, 64, 72, 96, 128, 136, 256])
+def test_attention_uses_the_pool_to_its_end(dim):
+    # a pool of exactly the pages in use, the last page full, right up to the end of its allocation
+    page, pages = 8, 24
+    gen = torch.Generator().manual_seed(dim)
+    k, v = (torch.randn(pages, 2, page, dim, generator=gen).to(BF) for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    for new in (1, 60):
+        q = torch.randn(new, 4, dim, generator=gen).to(BF)
+        out = qaff.paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), ints([0, new]), ints([pages * page]))
+        want, _, tol, _ = ref.attention(q, k, v, table, [0, new], [pages * page], 1 / math.sqrt(dim))
+        assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+def test_attention_without_a_pool():
+    # no page at all: every row that sees a key is NaN
+    k = torch.empty(0, 2, 16, 64, dtype=BF, device="cuda")
+    q = torch.randn(3, 4, 64, device="cuda").to(BF)
+    out = qaff.paged_attention(q, k, k.clone(), ints([[0, 1], [0, 0]]), ints([0, 1, 2]), ints([5, 0]))
+    assert out[0].isnan().all() and (out[1:] == 0).all()
+
+
 @pytest.mark.parametrize("dim", [64, 20])
 def test_attention_lengths_past_the_table(dim):
     # lengths that no table holds: NaN rows, and no time spent on keys that are not there
