@@ -482,15 +482,14 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int entry = (kt * KT + 16 * i + col) >> a.page_shift;
-            page[i] = table[min(entry, last_entry)];
-            if ((int64_t)min(kt * KT + 16 * i + col, hi_all - 1) >= a.table_keys) page[i] = -1;
+            page[i] = table[min(entry, last_entry)];  // looked at only by load_tile: no wait for it here
         }
     };
     auto load_tile = [&](int kt) {
         bad = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool ok = (uint32_t)page[i] < (uint64_t)a.pages;
+            const bool ok = (uint32_t)page[i] < (uint64_t)a.pages && min(kt * KT + 16 * i + col, hi_all - 1) < a.table_keys;
             if (!ok) bad |= 1 << i;
             const uint64_t at = (uint64_t)(uint32_t)(ok ? page[i] : 0) * (uint32_t)a.page_stride + head_at +
                                 (uint32_t)(((kt * KT + 16 * i + col) & page_mask) * dim);
@@ -721,11 +720,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     u32x4a kreg[PER], vreg[PER];
     auto load_pages = [&](int kt) {
         const int key = kt * KT + wave_row + RSTEP * min(lane, PER - 1);
-        pages = table[min(key >> a.page_shift, last_entry)];
-        if (min(key, hi_all - 1) >= a.table_keys) pages = -1;
+        pages = table[min(key >> a.page_shift, last_entry)];  // looked at only by load_tile: no wait for it here
     };
     auto load_tile = [&](int kt) {
-        const bool ok = (uint32_t)pages < (uint64_t)a.pages;
+        const int key = kt * KT + wave_row + RSTEP * min(lane, PER - 1);
+        const bool ok = (uint32_t)pages < (uint64_t)a.pages && min(key, hi_all - 1) < a.table_keys;
         bad = (uint32_t)__ballot(!ok);
         const int page = ok ? pages : 0;
 #pragma unroll
@@ -787,21 +786,47 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
         const int key0 = kt * KT;
         if (key0 >= any_hi) continue;  // keys past every row of this wave
 
+        // Reads from LDS go out four products ahead of those that take them: left to itself, the compiler
+        // reads an operand, waits and multiplies, and each wait is as long as four products. More ahead
+        // would not fit the registers.
+        constexpr int AHEAD = 4 / SB;  // depths of a stretch
+        op8<F16> kf[QF][SB];
+        auto read_keys = [&](int c0) {
+#pragma unroll
+            for (int c = c0; c < c0 + AHEAD; ++c)
+#pragma unroll
+                for (int kb = 0; kb < SB; ++kb) {
+                    const int row = kb * R + col;
+                    kf[c][kb] = *reinterpret_cast<const op8<F16>*>(
+                        kl + row * DP + (((2 * c + part) ^ swizzle_k<DP>(row)) * 8));
+                }
+        };
         acc_t sc[SB];
 #pragma unroll
         for (int kb = 0; kb < SB; ++kb)
 #pragma unroll
             for (int i = 0; i < VALS; ++i) sc[kb][i] = 0.f;
-        // blocks of keys inside: their products do not wait for each other
+        read_keys(0);
 #pragma unroll
-        for (int c = 0; c < QF; ++c)
+        for (int c0 = 0; c0 < QF; c0 += AHEAD) {
+            if (c0 + AHEAD < QF) read_keys(c0 + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+            // blocks of keys inside: their products do not wait for each other
 #pragma unroll
-            for (int kb = 0; kb < SB; ++kb) {
-                const int row = kb * R + col;
-                const op8<F16> kf = *reinterpret_cast<const op8<F16>*>(
-                    kl + row * DP + (((2 * c + part) ^ swizzle_k<DP>(row)) * 8));
-                sc[kb] = product<F16>(kf, q[c], sc[kb]);
+            for (int c = c0; c < c0 + AHEAD; ++c)
+#pragma unroll
+                for (int kb = 0; kb < SB; ++kb) sc[kb] = product<F16>(kf[c][kb], q[c], sc[kb]);
+        }
+        op8<F16> vf[2 * SB][OB];
+        auto read_values = [&](int f) {
+#pragma unroll
+            for (int n = 0; n < OB; ++n) {
+                uint16_t* src = vl + (v_row + 16 * f) * DP + ((v_piece + 4 * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
+                vf[f][n] = read_column<F16>(src, src + 8 * DP);
             }
+        };
+        read_values(0);
+        __builtin_amdgcn_sched_barrier(0);
         if (key0 < sure_lo || key0 + KT > sure_hi) mask_scores<R>(sc, key0, part, lo, hi);
         softmax_tile<F16, R>(sc, acc, factor, m, l);
         op8<F16> p[2 * SB];
@@ -813,12 +838,12 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
                                       __builtin_shufflevector(sc[f / 2], sc[f / 2], 4, 5, 6, 7));
         if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) again |= tile_not_finite<F16, TILE / 8>(vl);
 #pragma unroll
-        for (int f = 0; f < 2 * SB; ++f)
+        for (int f = 0; f < 2 * SB; ++f) {
+            if (f + 1 < 2 * SB) read_values(f + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = 0; n < OB; ++n) {
-                uint16_t* src = vl + (v_row + 16 * f) * DP + ((v_piece + 4 * n) ^ swizzle_v<DP, R>(v_row)) * 8 + v_sub;
-                acc[n] = product<F16>(read_column<F16>(src, src + 8 * DP), p[f], acc[n]);
-            }
+            for (int n = 0; n < OB; ++n) acc[n] = product<F16>(vf[f][n], p[f], acc[n]);
+        }
     }
 
     if (__any(again)) {  // this wave's rows
@@ -974,10 +999,11 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     }
     p.few.rows = kFewRows;
     p.many.rows = kManyRows;
-    // Few rows. Up to 1024 keys one workgroup of 8 waves takes them all, and there is nothing to join;
-    // beyond, 4 waves a workgroup and twice as many parts as workgroups fit the chip, so that uneven
-    // ends are short.
-    if (table_keys <= 1024) p.few_waves = 8;
+    // Few rows. A CU takes some 35 GB/s of keys and values whatever its waves (8 waves over 777 keys of 8
+    // heads: 16 us), so only up to 256 keys (a tile a wave) does one workgroup of 8 waves take them all,
+    // with nothing to join; beyond, 4 waves a workgroup and twice as many parts as workgroups fit the
+    // chip, so that uneven ends are short.
+    if (table_keys <= 256) p.few_waves = 8;
     p.few.cut(p.few_waves == 8 ? 0 : (cus * 4 + kv_heads - 1) / kv_heads, 4, table_keys, 32);
     // Many rows: cut only where whole tiles would leave workgroup slots (2 a CU) empty.
     const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
