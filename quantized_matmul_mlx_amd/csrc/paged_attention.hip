@@ -6,6 +6,7 @@
 // that the exponential is one v_exp_f32.
 #include "mfma16.h"
 #include "paged.h"
+#include "wave.h"
 
 namespace qaff {
 namespace {
@@ -153,24 +154,6 @@ struct Item {
     int b;
 };
 
-
-// One step of a scan in registers (no LDS round trip): v of the lane that the DPP control names, 0
-// where that lane is not there.
-template <int CTRL, int ROWS> __device__ __forceinline__ int dpp(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
-}
-// Inclusive sums over the wave's lanes: within rows of 16 lanes (row_shr 1, 2, 4, 8), then the last
-// lane of a row to the next rows (row_bcast 15 and 31).
-__device__ __forceinline__ int wave_scan(int v) {
-    v += dpp<0x111, 0xf>(v);
-    v += dpp<0x112, 0xf>(v);
-    v += dpp<0x114, 0xf>(v);
-    v += dpp<0x118, 0xf>(v);
-    v += dpp<0x142, 0xa>(v);
-    v += dpp<0x143, 0xc>(v);
-    return v;
-}
-__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
 // Every wave scans the requests itself, 64 at a time: with up to 63 requests that is one load of
@@ -434,17 +417,17 @@ __device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& i
 // addresses. A tile's keys are used before its values: their registers take the next tile's loads
 // at once, so a wave has about a tile (16 KB at 128 values) in flight all the time.
 constexpr int kFewRows = 16;
+template <int DP, int NS> constexpr int kFewLds = NS * (32 * DP * 2 + kFewRows * 8);
 template <bool F16, int DP, int NS, bool FULL>
-__global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(AttnArgs a, Sched s) {
-    constexpr int KT = 32, R = 16;
+__device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int block, uint8_t* lds) {
+    constexpr int KT = 32, R = kFewRows;
     constexpr int QF = DP / 32, OB = DP / 16;
     constexpr int BYTES = KT * DP * 2;  // of a wave: V's tile, then its rows' sums (16 rows of DP floats)
-    __shared__ __align__(16) uint8_t lds[NS][BYTES];
-    __shared__ float2 ml[NS][R];
+    float2* ml = reinterpret_cast<float2*>(lds + NS * BYTES);  // [wave][row]
 
     const int dim = FULL ? DP : a.dim;  // FULL: the head size is DP
-    const int hk = blockIdx.x % a.kv_heads;
-    const int item = blockIdx.x / a.kv_heads;
+    const int hk = block % a.kv_heads;
+    const int item = block / a.kv_heads;
     Item it;
     if (!find_item<R, KT>(a, s, item, false, it)) return;
 
@@ -549,7 +532,7 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
     float m = -INFINITY, l = 0.f;
     bool again = false;
     const float factor = a.scale * kLog2e;
-    uint16_t* vl = reinterpret_cast<uint16_t*>(lds[wave]);
+    uint16_t* vl = reinterpret_cast<uint16_t*>(lds + wave * BYTES);
     // a lane's transposing reads: rows v_row and v_row + 16, pieces 2 n + v_piece, from value v_sub on
     const int v_row = 4 * part + (col >> 2), v_piece = (lane & 3) >> 1, v_sub = 4 * (lane & 1);
 
@@ -600,25 +583,25 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 #pragma unroll
     for (int n = 0; n < OB; ++n) {
         const int d = 4 * n + part;
-        *reinterpret_cast<f32x4*>(lds[wave] + (16 * d + (col ^ (d & 15))) * 16) = acc[n];
+        *reinterpret_cast<f32x4*>(lds + wave * BYTES + (16 * d + (col ^ (d & 15))) * 16) = acc[n];
     }
-    if (part == 0) ml[wave][col] = make_float2(m - kLift<F16>, l);
+    if (part == 0) ml[wave * R + col] = make_float2(m - kLift<F16>, l);
     __syncthreads();
     const int64_t slot0 = ((int64_t)item * a.kv_heads + hk) * R;
     for (int u = tid; u < rows * (DP / 4); u += 64 * NS) {
         const int row = u / (DP / 4), d = u % (DP / 4);
-        float top = ml[0][row].x;
+        float top = ml[row].x;
 #pragma unroll
-        for (int w = 1; w < NS; ++w) top = fmaxf(top, ml[w][row].x);
+        for (int w = 1; w < NS; ++w) top = fmaxf(top, ml[w * R + row].x);
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < NS; ++w) {
-            const float2 x = ml[w][row];
+            const float2 x = ml[w * R + row];
             const float k = __builtin_amdgcn_exp2f(x.x - base);
             sum += k * x.y;
-            o += k * *reinterpret_cast<const f32x4*>(lds[w] + (16 * d + (row ^ (d & 15))) * 16);
+            o += k * *reinterpret_cast<const f32x4*>(lds + w * BYTES + (16 * d + (row ^ (d & 15))) * 16);
         }
         if (4 * d >= dim) continue;
         if (it.parts > 1) {
@@ -641,9 +624,11 @@ __global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(Att
 // Chunks and prompts: 4 waves of 32 rows. K and V tiles go through registers into LDS one tile ahead,
 // one barrier a tile.
 constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
-template <bool F16, int DP, int KT, bool FULL>
-__global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_kernel(AttnArgs a, Sched s) {
-    constexpr int R = 32, ROWS = kManyRows, NT = 64 * kManyWaves;
+template <int DP> constexpr int kManyKeys = DP > 128 ? 32 : 64;        // of a tile
+template <int DP> constexpr int kManyLds = 2 * 2 * kManyKeys<DP> * DP * 2;  // two buffers of K and V
+template <bool F16, int DP, bool FULL>
+__device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int block, uint8_t* lds_bytes) {
+    constexpr int R = 32, ROWS = kManyRows, NT = 64 * kManyWaves, KT = kManyKeys<DP>;
     constexpr int CH = DP / 8;               // 16-byte pieces of a row
     constexpr int PER = KT * CH / NT;        // pieces of a tile per thread, RSTEP rows apart
     constexpr int RSTEP = NT / CH;
@@ -651,11 +636,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     constexpr int VALS = Shape<R>::kVals;    // a lane's values of a product
     constexpr int QF = DP / 16, SB = KT / R, OB = DP / R;
     typedef typename Shape<R>::acc acc_t;
-    __shared__ __align__(16) uint16_t lds[2][2][TILE];
+    uint16_t* lds = reinterpret_cast<uint16_t*>(lds_bytes);
 
     const int dim = FULL ? DP : a.dim;
-    const int hk = blockIdx.x % a.kv_heads;
-    const int item = blockIdx.x / a.kv_heads;
+    const int hk = block % a.kv_heads;
+    const int item = block / a.kv_heads;
     Item it;
     if (!find_item<ROWS, KT>(a, s, item, false, it)) return;
 
@@ -769,8 +754,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     }
     for (int kt = kt_begin; kt < kt_end; ++kt) {
         if (dim < DP || kt * KT < lo_all || (kt + 1) * KT > hi_all || bad) fix_tile(kt);
-        uint16_t* kl = lds[kt & 1][0];
-        uint16_t* vl = lds[kt & 1][1];
+        uint16_t* kl = lds + (kt & 1) * 2 * TILE;
+        uint16_t* vl = kl + TILE;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int row = row0 + RSTEP * i;
@@ -884,19 +869,38 @@ __global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_k
     if (a.lse && part == 0) a.lse[row] = empty ? -INFINITY : (m_out + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+template <bool F16, int DP, int NS, bool FULL>
+__global__ __launch_bounds__(64 * NS, DP > 128 ? 1 : 2) void attn_few_kernel(AttnArgs a, Sched s) {
+    __shared__ __align__(16) uint8_t lds[kFewLds<DP, NS>];
+    few_rows<F16, DP, NS, FULL>(a, s, blockIdx.x, lds);
+}
+
+template <bool F16, int DP, bool FULL>
+__global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_many_kernel(AttnArgs a, Sched s) {
+    __shared__ __align__(16) uint8_t lds[kManyLds<DP>];
+    many_rows<F16, DP, FULL>(a, s, blockIdx.x, lds);
+}
+
+// Chunks or prompts beside decoding requests: both in one launch, the longer work first.
+template <bool F16, int DP, bool FULL>
+__global__ __launch_bounds__(64 * kManyWaves, DP > 128 ? 1 : 2) void attn_both_kernel(AttnArgs a, Sched many, Sched few,
+                                                                                     int many_blocks) {
+    __shared__ __align__(16) uint8_t lds[kManyLds<DP> > kFewLds<DP, kManyWaves> ? kManyLds<DP> : kFewLds<DP, kManyWaves>];
+    if ((int)blockIdx.x < many_blocks) many_rows<F16, DP, FULL>(a, many, blockIdx.x, lds);
+    else few_rows<F16, DP, kManyWaves, FULL>(a, few, (int)blockIdx.x - many_blocks, lds);
+}
+
 // Joins the parts of a tile's rows, in their order: o = sum_s w_s o_s / sum_s w_s l_s with
 // w_s = 2^(m_s - max m). A workgroup holds RP rows, DP / 4 threads each; the threads left over take
 // other parts of the same rows, up to kJoin parts at a time.
 constexpr int kJoin = 512;
 template <bool F16, int DP, int ROWS, int KT, int RP>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const Sched& s, int block, f32x4* so, float* weight) {
     constexpr int LANES = DP / 4, GROUPS = 256 / LANES / RP;
     static_assert(GROUPS >= 1 && (RP == 1 || GROUPS == 1), "");
-    __shared__ f32x4 so[GROUPS][LANES];
-    __shared__ float weight[RP][kJoin / RP];
-    const int hk = blockIdx.x % a.kv_heads;
+    const int hk = block % a.kv_heads;
     Item it;
-    if (!find_item<ROWS, KT>(a, s, blockIdx.x / a.kv_heads, true, it) || it.parts == 1) return;
+    if (!find_item<ROWS, KT>(a, s, block / a.kv_heads, true, it) || it.parts == 1) return;
     const int x = threadIdx.x % LANES, g = (threadIdx.x / LANES) % GROUPS, rp = threadIdx.x / (LANES * GROUPS);
     const int r0 = it.tile * ROWS, rows = min(ROWS, it.row_end - r0);
     const bool in = 4 * x < a.dim;
@@ -921,7 +925,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
                 const float2 ml = s.part_ml[slot0 + (p0 + p) * step];
                 const float w = __builtin_amdgcn_exp2f(ml.x - base);
                 sum += w * ml.y;
-                if (lane_of_row < 64) weight[rp][p] = w;
+                if (lane_of_row < 64) weight[rp * (kJoin / RP) + p] = w;
             }
             for (int y = min(64, LANES * GROUPS) / 2; y > 0; y >>= 1) sum += __shfl_xor(sum, y);
             __syncthreads();
@@ -933,15 +937,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
                 const float* src = s.part_o + (slot0 + (int64_t)p0 * step) * a.dim + 4 * x;
 #pragma unroll 8
                 for (int p = g; p < n; p += GROUPS)
-                    o += weight[rp][p] * *reinterpret_cast<const f32x4*>(src + p * step * a.dim);
+                    o += weight[rp * (kJoin / RP) + p] * *reinterpret_cast<const f32x4*>(src + p * step * a.dim);
             }
         }
         if (GROUPS > 1) {
             __syncthreads();
-            so[g][x] = o;
+            so[g * LANES + x] = o;
             __syncthreads();
             if (g == 0)
-                for (int p = 1; p < GROUPS; ++p) o += so[p][x];
+                for (int p = 1; p < GROUPS; ++p) o += so[p * LANES + x];
         }
         if (g != 0 || rb + rp >= rows) continue;
         const int token = (r0 + r) / a.group, head = hk * a.group + (r0 + r) - token * a.group;
@@ -955,6 +959,18 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched s) {
                 make_uint2(pack_half2<F16>(o.x * inv, o.y * inv), pack_half2<F16>(o.z * inv, o.w * inv));
         if (a.lse && x == 0) a.lse[row] = empty ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
     }
+}
+
+// The joins of both kernels' tiles: the many-rows kernel's (8 rows of 128 values a workgroup), then the
+// few-rows kernel's (a row a workgroup, its parts spread over the threads).
+template <bool F16, int DP>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched many, Sched few, int many_blocks) {
+    __shared__ f32x4 so[256];
+    __shared__ float weight[kJoin];
+    if ((int)blockIdx.x < many_blocks)
+        join_rows<F16, DP, kManyRows, kManyKeys<DP>, 1024 / DP>(a, many, blockIdx.x, so, weight);
+    else
+        join_rows<F16, DP, kFewRows, 32, 1>(a, few, (int)blockIdx.x - many_blocks, so, weight);
 }
 
 // How a call runs: the few-rows kernel, the many-rows kernel or both, and whether their tiles are cut
@@ -988,7 +1004,10 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
         p.few.tiles = holders + rows / kFewRows;
         p.few.rows_hi = 0x7fffffff;
     } else {
-        if (requests > 1) {
+        // Of up to 4 requests with a chunk among them, the others may as well run with the chunks (one row
+        // in a tile of 128, its keys cut into parts like theirs): looking for them in a kernel of their
+        // own, and for their parts in a join, took 5 us where there were none.
+        if (requests > 4) {
             p.few.tiles = kFewMax / kFewRows * holders;
             p.few.rows_hi = kFewMax;
             p.many.rows_lo = kFewMax;
@@ -1003,39 +1022,39 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     // heads: 16 us), so only up to 256 keys (a tile a wave) does one workgroup of 8 waves take them all,
     // with nothing to join; beyond, 4 waves a workgroup and twice as many parts as workgroups fit the
     // chip, so that uneven ends are short.
-    if (table_keys <= 256) p.few_waves = 8;
+    if (table_keys <= 256 && !p.many.tiles) p.few_waves = 8;
     p.few.cut(p.few_waves == 8 ? 0 : (cus * 4 + kv_heads - 1) / kv_heads, 4, table_keys, 32);
     // Many rows: cut only where whole tiles would leave workgroup slots (2 a CU) empty.
     const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
-    const int tile = head_dim > 128 ? 32 : 64;
+    const int tile = head_dim > 128 ? kManyKeys<256> : kManyKeys<128>;
     p.many.cut(p.many.tiles < slots ? 2 * slots : 0, 512 / tile, table_keys, tile);
     return p;
 }
 
 template <bool F16, int DP, bool FULL>
 hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream) {
-    constexpr int KT = DP > 128 ? 32 : 64;
-    constexpr int RP = 1024 / DP;
     const size_t few_slots = p.few.slots(a.kv_heads), many_slots = p.many.slots(a.kv_heads);
     float* o = a.partial;
     float2* ml = reinterpret_cast<float2*>(o + (few_slots + many_slots) * a.dim);
     const Sched few{p.few.rows_lo, p.few.rows_hi, p.few.parts, p.few.min_part, o, ml};
     const Sched many{p.many.rows_lo, p.many.rows_hi, p.many.parts, p.many.min_part, o + few_slots * a.dim, ml + few_slots};
-    if (p.many.tiles)
-        attn_many_kernel<F16, DP, KT, FULL><<<(unsigned)(p.many.items * a.kv_heads), 64 * kManyWaves, 0, stream>>>(a, many);
-    if (p.few.tiles) {
-        const unsigned grid = (unsigned)(p.few.items * a.kv_heads);
-        // (heads above 128 need more registers than 8 waves a workgroup can have)
-        constexpr int kWide = DP > 128 ? 4 : 8;
-        if (p.few_waves == 8) attn_few_kernel<F16, DP, kWide, FULL><<<grid, 64 * kWide, 0, stream>>>(a, few);
-        else attn_few_kernel<F16, DP, 4, FULL><<<grid, 256, 0, stream>>>(a, few);
+    const unsigned few_blocks = (unsigned)(p.few.items * a.kv_heads), many_blocks = (unsigned)(p.many.items * a.kv_heads);
+    constexpr int kWide = DP > 128 ? 4 : 8;  // heads above 128 need more registers than 8 waves can have
+    if (p.many.tiles && p.few.tiles)
+        attn_both_kernel<F16, DP, FULL><<<many_blocks + few_blocks, 256, 0, stream>>>(a, many, few, (int)many_blocks);
+    else if (p.many.tiles)
+        attn_many_kernel<F16, DP, FULL><<<many_blocks, 256, 0, stream>>>(a, many);
+    else if (p.few_waves == 8)
+        attn_few_kernel<F16, DP, kWide, FULL><<<few_blocks, 64 * kWide, 0, stream>>>(a, few);
+    else
+        attn_few_kernel<F16, DP, 4, FULL><<<few_blocks, 256, 0, stream>>>(a, few);
+    if (p.many.parts || p.few.parts) {
+        const unsigned many_tiles = p.many.parts ? (unsigned)(p.many.tiles * a.kv_heads) : 0;
+        const unsigned few_tiles = p.few.parts ? (unsigned)(p.few.tiles * a.kv_heads) : 0;
+        const unsigned few_y = a.group < kFewRows ? a.group : kFewRows;
+        join_kernel<F16, DP><<<dim3(many_tiles + few_tiles, many_tiles ? kManyRows * DP / 1024 : few_y), 256, 0, stream>>>(
+            a, many, few, (int)many_tiles);
     }
-    if (p.many.parts)
-        join_kernel<F16, DP, kManyRows, KT, RP>
-            <<<dim3((unsigned)(p.many.tiles * a.kv_heads), kManyRows / RP), 256, 0, stream>>>(a, many);
-    if (p.few.parts)
-        join_kernel<F16, DP, kFewRows, 32, 1>
-            <<<dim3((unsigned)(p.few.tiles * a.kv_heads), a.group < kFewRows ? a.group : kFewRows), 256, 0, stream>>>(a, few);
     return hipGetLastError();
 }
 

@@ -6,6 +6,7 @@
 // instead of waiting for another kernel's scan, then each thread finds one token's request by a
 // binary search in LDS.
 #include "paged.h"
+#include "wave.h"
 
 namespace qaff {
 namespace {
@@ -14,17 +15,6 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanWaves = kPlanThreads / 64;
 
 __device__ __forceinline__ int32_t saturated(int64_t v) { return v > 0x7fffffff ? 0x7fffffff : (int32_t)v; }
-
-// Inclusive sum over the wave's lanes.
-__device__ __forceinline__ int64_t wave_scan(int64_t v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t u = __shfl_up(v, d);
-        if (lane >= d) v += u;
-    }
-    return v;
-}
 
 __global__ __launch_bounds__(kPlanThreads) void paged_plan_kernel(PlanArgs a) {
     extern __shared__ int32_t lds[];
