@@ -156,23 +156,19 @@ struct Item {
 
 
 // Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
-// Every wave scans the requests itself, 64 at a time: with up to 63 requests that is one load of
-// each length and two scans, less than reading another kernel's schedule would cost. Rows past the
-// last request are one more request without keys.
+// Every wave scans the requests itself, 64 at a time: with up to 64 requests that is one load of
+// each length and two scans, less than reading another kernel's schedule would cost.
 template <int ROWS, int KT>
 __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_tile, Item& it) {
     const int lane = threadIdx.x & 63;
-    const int count = a.requests + 1;
+    const int count = a.requests;
     int start = 0, end = 0, kv = 0, tiles = 0, span = 0;
     auto load = [&](int b) {
         start = end = kv = tiles = span = 0;
-        if (b < a.requests) {
+        if (b < count) {
             start = a.cu[b];
             end = a.cu[b + 1];
             kv = a.kv_lens[b];
-        } else if (b == a.requests) {
-            start = a.cu[b];
-            end = a.tokens;
         }
         kv = max(kv, 0);
         if (start >= 0 && end > start && end <= a.tokens) {
@@ -188,7 +184,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
     uint32_t len = 0x7fffffffu;  // key tiles of a part
     if (s.parts > 0) {
         // tiles times spans; where 32 bits might not hold the sum, nothing is cut
-        const uint32_t cap = 0x7fffffffu / (uint32_t)count;
+        const uint32_t cap = 0x7fffffffu / (uint32_t)max(count, 1);
         bool past_cap = false;
         auto product = [&] {
             const uint64_t x = (uint64_t)(uint32_t)tiles * (uint32_t)span;
@@ -228,9 +224,24 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
         }
         items_before = lane_value(items_in, 63);
         tiles_before = lane_value(tiles_in, 63);
-        if (b0 + 64 >= count) return false;
+        if (b0 + 64 >= count) break;
         load(b0 + 64 + lane);
     }
+    // rows past the last request: one more request, without keys
+    it.start = a.cu[count];
+    it.end = a.tokens;
+    it.row_end = it.start >= 0 && it.start < it.end ? (it.end - it.start) * a.group : 0;
+    if (it.row_end <= s.rows_lo || it.row_end > s.rows_hi) return false;
+    const int t = (int)(((uint32_t)it.row_end + ROWS - 1) / ROWS);
+    const int local = want - (by_tile ? tiles_before : items_before);
+    if (local >= t) return false;
+    it.first = items_before + local;
+    it.part = 0;
+    it.parts = 1;
+    it.tile = t - 1 - local;
+    it.kv = 0;
+    it.b = count;
+    return true;
 }
 
 // Key tiles [begin, end) of an item's part, of n from tile t0 on: the first n % parts are one longer.
@@ -696,8 +707,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* table = a.tables + (int64_t)it.b * a.table_width;
     const int last_entry = min(max(hi_all, 1) - 1, a.table_keys - 1) >> a.page_shift;
-    const int64_t head_at = ((int64_t)hk << a.page_shift) * dim;
-    const uint32_t lane_at = (uint32_t)((row0 - wave_row) * dim + (piece * 8 < dim ? piece * 8 : 0));
+    const uint32_t lane_at = (uint32_t)((row0 - wave_row) * dim + (piece * 8 < dim ? piece * 8 : 0)) * 2;  // bytes
     // As in the other kernel, loads need no condition and are put right before their use. Lane i of
     // `pages` holds the page of row wave_row + RSTEP i of the tile that is loaded next.
     int pages;
@@ -711,13 +721,15 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int
         const int key = kt * KT + wave_row + RSTEP * min(lane, PER - 1);
         const bool ok = (uint32_t)pages < (uint64_t)a.pages && min(key, hi_all - 1) < a.table_keys;
         bad = (uint32_t)__ballot(!ok);
-        const int page = ok ? pages : 0;
+        // where that row lies in the caches, in bytes
+        const uint64_t row_at = 2 * ((uint64_t)(uint32_t)(ok ? pages : 0) * (uint32_t)a.page_stride +
+                                     (((uint64_t)hk << a.page_shift) + (key & page_mask)) * dim);
+        const int at_lo = (int)(uint32_t)row_at, at_hi = (int)(row_at >> 32);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int64_t at = (int64_t)((uint64_t)(uint32_t)lane_value(page, i) * (uint32_t)a.page_stride) + head_at +
-                               (int64_t)((kt * KT + wave_row + RSTEP * i) & page_mask) * dim;
-            kreg[i] = *reinterpret_cast<const u32x4a*>(a.k_cache + at + lane_at);
-            vreg[i] = *reinterpret_cast<const u32x4a*>(a.v_cache + at + lane_at);
+            const uint64_t at = (uint64_t)(uint32_t)lane_value(at_hi, i) << 32 | (uint32_t)lane_value(at_lo, i);
+            kreg[i] = *reinterpret_cast<const u32x4a*>(reinterpret_cast<const uint8_t*>(a.k_cache) + at + lane_at);
+            vreg[i] = *reinterpret_cast<const u32x4a*>(reinterpret_cast<const uint8_t*>(a.v_cache) + at + lane_at);
         }
     };
     auto fix_tile = [&](int kt) {
@@ -752,6 +764,10 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int
         load_tile(kt_begin);
         load_pages(kt_begin + 1);
     }
+    // Products and loads go before the other wave's softmax on the SIMD: both waves at their products would
+    // wait for each other, while one at its products and one at its softmax do not (595 -> 583 us for a prompt
+    // of 8192, 330 -> 313 us for 512 tokens over 32768).
+    __builtin_amdgcn_s_setprio(1);
     for (int kt = kt_begin; kt < kt_end; ++kt) {
         if (dim < DP || kt * KT < lo_all || (kt + 1) * KT > hi_all || bad) fix_tile(kt);
         uint16_t* kl = lds + (kt & 1) * 2 * TILE;
@@ -812,6 +828,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int
         };
         read_values(0);
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(0);
         if (key0 < sure_lo || key0 + KT > sure_hi) mask_scores<R>(sc, key0, part, lo, hi);
         softmax_tile<F16, R>(sc, acc, factor, m, l);
         op8<F16> p[2 * SB];
@@ -822,6 +839,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int
                          : pack8<F16>(__builtin_shufflevector(sc[f / 2], sc[f / 2], 0, 1, 2, 3),
                                       __builtin_shufflevector(sc[f / 2], sc[f / 2], 4, 5, 6, 7));
         if (key0 < sure_lo || min(key0 + KT, hi_all) > sure_hi) again |= tile_not_finite<F16, TILE / 8>(vl);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int f = 0; f < 2 * SB; ++f) {
             if (f + 1 < 2 * SB) read_values(f + 1);
@@ -962,15 +980,15 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Sched& s, int
 }
 
 // The joins of both kernels' tiles: the many-rows kernel's (8 rows of 128 values a workgroup), then the
-// few-rows kernel's (a row a workgroup, its parts spread over the threads).
-template <bool F16, int DP>
+// few-rows kernel's (RP rows a workgroup).
+template <bool F16, int DP, int RP>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched many, Sched few, int many_blocks) {
     __shared__ f32x4 so[256];
     __shared__ float weight[kJoin];
     if ((int)blockIdx.x < many_blocks)
         join_rows<F16, DP, kManyRows, kManyKeys<DP>, 1024 / DP>(a, many, blockIdx.x, so, weight);
     else
-        join_rows<F16, DP, kFewRows, 32, 1>(a, few, (int)blockIdx.x - many_blocks, so, weight);
+        join_rows<F16, DP, kFewRows, 32, RP>(a, few, (int)blockIdx.x - many_blocks, so, weight);
 }
 
 // How a call runs: the few-rows kernel, the many-rows kernel or both, and whether their tiles are cut
@@ -1023,11 +1041,15 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     // with nothing to join; beyond, 4 waves a workgroup and twice as many parts as workgroups fit the
     // chip, so that uneven ends are short.
     if (table_keys <= 256 && !p.many.tiles) p.few_waves = 8;
-    p.few.cut(p.few_waves == 8 ? 0 : (cus * 4 + kv_heads - 1) / kv_heads, 4, table_keys, 32);
-    // Many rows: cut only where whole tiles would leave workgroup slots (2 a CU) empty.
-    const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;
+    // Beside the many-rows kernel's workgroups, which fill the chip, once is enough (two chunks and 31
+    // decoding requests: 45.0 -> 42.4 us).
+    const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;  // workgroups that run at once, of a cache head
+    p.few.cut(p.few_waves == 8 ? 0 : p.many.tiles ? slots : 2 * slots, 4, table_keys, 32);
+    // Many rows: cut only where whole tiles would leave slots empty, into as many parts as there are slots:
+    // twice as many cost more in partial sums (512 tokens over 32768: 38 MB) than even ends gain (322
+    // against 309 us; over short caches 27.6 against 28.1).
     const int tile = head_dim > 128 ? kManyKeys<256> : kManyKeys<128>;
-    p.many.cut(p.many.tiles < slots ? 2 * slots : 0, 512 / tile, table_keys, tile);
+    p.many.cut(p.many.tiles < slots ? slots : 0, 512 / tile, table_keys, tile);
     return p;
 }
 
@@ -1051,9 +1073,18 @@ hipError_t launch_tiles(const AttnArgs& a, const Launches& p, hipStream_t stream
     if (p.many.parts || p.few.parts) {
         const unsigned many_tiles = p.many.parts ? (unsigned)(p.many.tiles * a.kv_heads) : 0;
         const unsigned few_tiles = p.few.parts ? (unsigned)(p.few.tiles * a.kv_heads) : 0;
-        const unsigned few_y = a.group < kFewRows ? a.group : kFewRows;
-        join_kernel<F16, DP><<<dim3(many_tiles + few_tiles, many_tiles ? kManyRows * DP / 1024 : few_y), 256, 0, stream>>>(
-            a, many, few, (int)many_tiles);
+        // A row a workgroup, its parts spread over the threads, where a tile has many parts (two rows over
+        // 120001 keys); several rows a workgroup, so fewer workgroups to look for their tile, otherwise (64
+        // decoding requests: the two kernels 215 -> 209 us).
+        const int few_rows = a.group < kFewRows ? a.group : kFewRows;
+        constexpr int RP = 1024 / DP;
+        if (p.few.parts >= 4 * p.few.tiles) {
+            const dim3 grid(many_tiles + few_tiles, many_tiles ? kManyRows / RP : few_rows);
+            join_kernel<F16, DP, 1><<<grid, 256, 0, stream>>>(a, many, few, (int)many_tiles);
+        } else {
+            const dim3 grid(many_tiles + few_tiles, many_tiles ? kManyRows / RP : (few_rows + RP - 1) / RP);
+            join_kernel<F16, DP, RP><<<grid, 256, 0, stream>>>(a, many, few, (int)many_tiles);
+        }
     }
     return hipGetLastError();
 }
