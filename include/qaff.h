@@ -428,7 +428,8 @@ qaff_status qaff_paged_plan(const int32_t* cached_lens, const int32_t* new_lens,
  * Float32 arithmetic, rounded to nearest even once at the end.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, odd rot, rot above head_dim, axes
  * outside 1 to 4, sections that do not fit, negative strides, null or misaligned pointers;
- * UNSUPPORTED for a page size not listed above, head_dim above 512, or 2^31 tokens or more.
+ * UNSUPPORTED for a page size not listed above, head_dim above 512, 2^31 tokens or more, or more
+ * tokens than one launch holds (2^24).
  */
 qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_dtype dtype, int64_t tokens,
                              int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t q_token_stride,

@@ -28,6 +28,8 @@ qaff_status after_launch(const char* op, hipError_t e, hipStream_t stream) {
         const char* v = std::getenv("QAFF_DEBUG_SYNC");
         return v && v[0] && std::strcmp(v, "0") != 0;
     }();
+    if (e == hipErrorInvalidConfiguration)
+        return fail(QAFF_ERR_UNSUPPORTED, "%s: more rows than one launch holds (2^32 threads)", op);
     if (e == hipSuccess && sync) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return fail(QAFF_ERR_DEVICE, "%s: %s", op, hipGetErrorString(e));
     return QAFF_OK;

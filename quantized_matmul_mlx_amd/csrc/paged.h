@@ -12,6 +12,10 @@ namespace qaff {
 void set_error(const char* text) noexcept;
 int device_cu_count();
 
+// Whether `blocks` workgroups of `threads` fit one launch (fewer than 2^32 threads); a launcher whose
+// grid does not returns hipErrorInvalidConfiguration before any launch.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks < (1LL << 32) / threads; }
+
 constexpr int64_t kPlanMaxRequests = 16384;
 
 struct PlanArgs {

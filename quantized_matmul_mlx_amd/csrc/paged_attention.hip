@@ -1111,12 +1111,15 @@ hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, 
                         a.page_stride < (1LL << 32) && a.pages > 0 && a.table_keys > 0 &&
                         aligned16(a.q) && aligned16(a.k_cache) && aligned16(a.v_cache) && aligned16(a.out);
     if (!pieces) {
+        if (!grid_fits((int64_t)a.tokens * a.heads, 64)) return hipErrorInvalidConfiguration;
         const unsigned grid = (unsigned)a.tokens * (unsigned)a.heads;
         if (f16) attn_scalar_kernel<true><<<grid, 64, 0, stream>>>(a);
         else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
     const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_keys, a.requests, max_new);
+    if (!grid_fits((p.few.items + p.many.items) * a.kv_heads, 512) || !grid_fits((p.few.tiles + p.many.tiles) * a.kv_heads, 256))
+        return hipErrorInvalidConfiguration;
     if (a.dim <= 64) return f16 ? launch_dim<true, 64>(a, p, stream) : launch_dim<false, 64>(a, p, stream);
     if (a.dim <= 128) return f16 ? launch_dim<true, 128>(a, p, stream) : launch_dim<false, 128>(a, p, stream);
     return f16 ? launch_dim<true, 256>(a, p, stream) : launch_dim<false, 256>(a, p, stream);

@@ -181,11 +181,12 @@ hipError_t launch_rope_append(const RopeArgs& a, bool f16, bool traditional, hip
                         aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.k_cache) &&
                         aligned16(a.v_cache) && aligned16(a.q_out);
     const int64_t units = (int64_t)(a.heads + 2 * a.kv_heads) * (a.dim / 8);
-    if (pieces && a.tokens * (units / kRopeThreads + 1) < (1LL << 31)) {
+    if (pieces && grid_fits(a.tokens * (units / kRopeThreads + 1), kRopeThreads)) {
         if (f16) traditional ? launch_pieces<true, true>(a, stream) : launch_pieces<true, false>(a, stream);
         else traditional ? launch_pieces<false, true>(a, stream) : launch_pieces<false, false>(a, stream);
         return hipGetLastError();
     }
+    if (!grid_fits(a.tokens, kRopeThreads)) return hipErrorInvalidConfiguration;
     const unsigned grid = (unsigned)a.tokens;
     if (f16) rope_scalar_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a, traditional);
     else rope_scalar_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a, traditional);

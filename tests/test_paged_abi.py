@@ -117,6 +117,15 @@ def test_attention_unsupported_and_no_ops(lib):
     assert attention(lib, heads=0, kv_heads=0, q=None, out=None) == OK
 
 
+def test_grids_that_no_launch_holds(lib):
+    # 2^32 threads or more: refused before any launch
+    assert rope(lib, tokens=2**24) == UNSUPPORTED                                       # a workgroup of 256 a token
+    assert rope(lib, tokens=2**24, dim=62, rot=62, q_ts=248, q_hs=62) == UNSUPPORTED    # element by element
+    assert b"2^32" in lib.qaff_last_error()
+    assert attention(lib, tokens=2**24, dim=62, q_ts=248, q_hs=62) == UNSUPPORTED       # a wave a row
+    assert b"2^32" in lib.qaff_last_error()
+
+
 def test_attention_workspace(lib):
     size = lib.qaff_paged_attention_workspace_size
     for bad in ((-1, 8, 2, 64, 16, 3, 2, 1), (3, 8, 3, 64, 16, 3, 2, 1), (3, 8, 2, 300, 16, 3, 2, 1),
