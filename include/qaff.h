@@ -466,7 +466,8 @@ qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_d
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, heads not a multiple of kv_heads, a
  * scale that is not positive and finite, null or misaligned pointers, a short workspace; UNSUPPORTED
  * for a page size not listed above, head_dim above 256, more than 65536 requests, tokens * heads of
- * 2^31 or more, or a table of 2^30 tokens or more a request.
+ * 2^31 or more, more rows than one launch holds (2^26 for head sizes and alignments without 16-byte
+ * pieces), or a table of 2^30 tokens or more a request.
  */
 qaff_status qaff_paged_attention(const void* q, qaff_dtype dtype, int64_t tokens, int64_t heads,
                                  int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,

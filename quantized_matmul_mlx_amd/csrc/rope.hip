@@ -80,7 +80,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_scalar_kernel(RopeArgs a, i
 
 // 16 bytes at a time. A thread's unit is a piece of 8 values, or the two pieces whose values turn
 // together (values i and i + half). The loads do not wait for the angles: every thread first asks for
-// its units, then the workgroup computes the token's angles, then the units turn and go out.
+// its units, then the workgroup computes the token's angles, then the units turn and go out. 8192 tokens
+// of 32 + 8 + 8 heads of 128: 41.6 us, 4.83 TB/s, a large copy's rate; two units a thread keep enough
+// loads on their way, one starts sooner where there are few (64 tokens: 3.0 us).
 template <bool F16, bool TRADITIONAL, int UNITS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int blocks_per_token) {
     __shared__ float2 turn[256];
