@@ -450,8 +450,8 @@ qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_d
  *   does a row past cu_new[requests]. Values and keys that a token does not see do not enter its row,
  *   whatever they hold.
  *   q [tokens, heads, head_dim] with token and head strides in elements (the last axis contiguous);
- *   block_tables int32 [requests, table_width]; cu_new int32 [requests + 1]; kv_lens int32
- *   [requests]; out [tokens, heads, head_dim] contiguous; lse float32 [tokens, heads] or null: the
+ *   block_tables int32 [requests, table_width]; cu_new int32 [requests + 1], from 0 on and not
+ *   decreasing; kv_lens int32 [requests]; out [tokens, heads, head_dim] contiguous; lse float32 [tokens, heads] or null: the
  *   natural logarithm of the sum of exponentials of the scaled scores.
  *   max_new: the largest number of new tokens of any request, or any bound of it: a hint for the
  *   choice of kernel. scale > 0.

@@ -424,6 +424,17 @@ def test_attention_many_requests():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("requests", [1, 63, 64, 65, 128, 129])
+@pytest.mark.parametrize("new", [1, 50])
+def test_attention_requests_and_rows_past_them(requests, new):
+    # the search for a row's request takes 64 requests at a time; rows past the last are zeros
+    banner(f"attention {requests} requests of {new}")
+    rng = random.Random(requests)
+    c = Case([(rng.randint(new, 200), new if b % 9 == 0 else 1) for b in range(requests)], 4, 2, 64, 16, BF, pad_rows=70)
+    c.check(c.run())
+    c.check(c.run(max_new=max(new, 70)))
+
+
 def test_attention_same_bits_each_time_and_on_another_stream():
     c = Case([(3000, 1), (900, 33), (40, 40)], 8, 2, 128, 16, BF)
     k, v = c.caches()
