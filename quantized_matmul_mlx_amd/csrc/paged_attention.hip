@@ -427,7 +427,7 @@ __device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& i
 // instruction, a lane's 2 rows the same for K and V, so a tile costs it 2 table lookups and 2
 // addresses. A tile's keys are used before its values: their registers take the next tile's loads
 // at once, so a wave has about a tile (16 KB at 128 values) in flight all the time. Memory bounds it: 64
-// decoding requests of up to 8192 keys take 209 us with the join, 5.19 TB/s (a large copy: 5.0).
+// decoding requests of up to 8192 keys take 203 us with the join, 5.34 TB/s (a large copy: 5.0).
 constexpr int kFewRows = 16;
 template <int DP, int NS> constexpr int kFewLds = NS * (32 * DP * 2 + kFewRows * 8);
 template <bool F16, int DP, int NS, bool FULL>
@@ -634,7 +634,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int 
 }
 
 // Chunks and prompts: 4 waves of 32 rows. K and V tiles go through registers into LDS one tile ahead,
-// one barrier a tile. A prompt of 8192 (32 heads of 128): 562 to 579 us, 950 to 977 TFLOP/s; the matrix
+// one barrier a tile. A prompt of 8192 (32 heads of 128): 562 to 585 us, 940 to 977 TFLOP/s; the matrix
 // cores are busy 44% of the time and the vector units 47%, which bounds it: the softmax, the tiles'
 // addresses and LDS accesses take as many issue slots as the products take cycles. Interleaving the
 // products with another tile's softmax within a wave, and loads straight into LDS, gave the same time.
@@ -1043,12 +1043,15 @@ Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t 
     // Few rows. A CU takes some 35 GB/s of keys and values whatever its waves (8 waves over 777 keys of 8
     // heads: 16 us), so only up to 256 keys (a tile a wave) does one workgroup of 8 waves take them all,
     // with nothing to join; beyond, 4 waves a workgroup and twice as many parts as workgroups fit the
-    // chip, so that uneven ends are short.
+    // chip, so that uneven ends are short (two rows over 120001 keys: 126 us, 152 with once as many).
     if (table_keys <= 256 && !p.many.tiles) p.few_waves = 8;
     // Beside the many-rows kernel's workgroups, which fill the chip, once is enough (two chunks and 31
     // decoding requests: 45.0 -> 42.4 us).
     const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;  // workgroups that run at once, of a cache head
-    p.few.cut(p.few_waves == 8 ? 0 : p.many.tiles ? slots : 2 * slots, 4, table_keys, 32);
+    // Many requests over long tables end unevenly: three times the slots (64 requests of up to 8192 keys: 209
+    // -> 203 us, 128 of them 443 -> 439); over short tables the joins cost more (64 of up to 1500: 57 -> 60).
+    const int64_t times = p.many.tiles ? 1 : p.few.tiles > slots / 2 && table_keys >= 4096 ? 3 : 2;
+    p.few.cut(p.few_waves == 8 ? 0 : times * slots, 4, table_keys, 32);
     // Many rows: cut only where whole tiles would leave slots empty, into as many parts as there are slots:
     // twice as many cost more in partial sums (512 tokens over 32768: 38 MB) than even ends gain (322
     // against 309 us; over short caches 27.6 against 28.1).
