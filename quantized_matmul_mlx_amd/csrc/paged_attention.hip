@@ -6,6 +6,7 @@
 // that the exponential is one v_exp_f32.
 #include "mfma16.h"
 #include "paged.h"
+#include "paged_sched.h"
 #include "wave.h"
 
 namespace qaff {
@@ -173,18 +174,15 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
         kv = max(kv, 0);
         if (start >= 0 && end > start && end <= a.tokens) {
             const int rows = (end - start) * a.group;  // at most tokens * heads < 2^31
-            if (rows > s.rows_lo && rows <= s.rows_hi) tiles = (int)(((uint32_t)rows + ROWS - 1) / ROWS);
+            tiles = tiles_of(rows, ROWS, s.rows_lo, s.rows_hi);
         }
-        // key tiles that a tile's rows see: all, or with a window that and the tokens a tile may touch
-        const uint32_t window = (uint32_t)min(a.window, (int64_t)0x3fffffff) + (uint32_t)(ROWS / a.group + 2 + KT);
-        const uint32_t keys = a.window > 0 ? min((uint32_t)kv, window) : (uint32_t)kv;
-        span = (int)((min(keys, (uint32_t)a.table_keys) + KT - 1) / KT);
+        span = span_of(kv, a.window, a.table_keys, a.group, ROWS, KT);
     };
     load(lane);
     uint32_t len = 0x7fffffffu;  // key tiles of a part
     if (s.parts > 0) {
         // tiles times spans; where 32 bits might not hold the sum, nothing is cut
-        const uint32_t cap = 0x7fffffffu / (uint32_t)max(count, 1);
+        const uint32_t cap = work_cap(count);
         bool past_cap = false;
         auto product = [&] {
             const uint64_t x = (uint64_t)(uint32_t)tiles * (uint32_t)span;
@@ -197,12 +195,12 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
             total += product();
         }
         const uint32_t all = (uint32_t)lane_value(wave_scan(total), 63);
-        if (!__any(past_cap)) len = max((uint32_t)s.min_part, (all + (uint32_t)s.parts - 1) / (uint32_t)s.parts);
+        if (!__any(past_cap)) len = part_length(all, s.parts, s.min_part);
         if (count > 64) load(lane);
     }
     int items_before = 0, tiles_before = 0;
     for (int b0 = 0;; b0 += 64) {
-        const int parts = max(1, (int)(((uint32_t)span + len - 1) / len));
+        const int parts = parts_of(span, len);
         const int items = tiles * parts;
         const int items_in = items_before + wave_scan(items), tiles_in = tiles_before + wave_scan(tiles);
         const uint64_t past = __ballot((by_tile ? tiles_in : items_in) > want);
@@ -428,11 +426,10 @@ __device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& i
 // addresses. A tile's keys are used before its values: their registers take the next tile's loads
 // at once, so a wave has about a tile (16 KB at 128 values) in flight all the time. Memory bounds it: 64
 // decoding requests of up to 8192 keys take 203 us with the join, 5.34 TB/s (a large copy: 5.0).
-constexpr int kFewRows = 16;
 template <int DP, int NS> constexpr int kFewLds = NS * (32 * DP * 2 + kFewRows * 8);
 template <bool F16, int DP, int NS, bool FULL>
 __device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int block, uint8_t* lds) {
-    constexpr int KT = 32, R = kFewRows;
+    constexpr int KT = kFewKeys, R = kFewRows;
     constexpr int QF = DP / 32, OB = DP / 16;
     constexpr int BYTES = KT * DP * 2;  // of a wave: V's tile, then its rows' sums (16 rows of DP floats)
     float2* ml = reinterpret_cast<float2*>(lds + NS * BYTES);  // [wave][row]
@@ -638,8 +635,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int 
 // cores are busy 44% of the time and the vector units 47%, which bounds it: the softmax, the tiles'
 // addresses and LDS accesses take as many issue slots as the products take cycles. Interleaving the
 // products with another tile's softmax within a wave, and loads straight into LDS, gave the same time.
-constexpr int kManyWaves = 4, kManyRows = 32 * kManyWaves;
-template <int DP> constexpr int kManyKeys = DP > 128 ? 32 : 64;        // of a tile
+constexpr int kManyWaves = kManyRows / 32;
+template <int DP> constexpr int kManyKeys = many_keys(DP);
 template <int DP> constexpr int kManyLds = 2 * 2 * kManyKeys<DP> * DP * 2;  // two buffers of K and V
 template <bool F16, int DP, bool FULL>
 __device__ __forceinline__ void many_rows(const AttnArgs& a, const Sched& s, int block, uint8_t* lds_bytes) {
@@ -992,72 +989,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, Sched many, Sched
     if ((int)blockIdx.x < many_blocks)
         join_rows<F16, DP, kManyRows, kManyKeys<DP>, 1024 / DP>(a, many, blockIdx.x, so, weight);
     else
-        join_rows<F16, DP, kFewRows, 32, RP>(a, few, (int)blockIdx.x - many_blocks, so, weight);
-}
-
-// How a call runs: the few-rows kernel, the many-rows kernel or both, and whether their tiles are cut
-// along the keys.
-constexpr int kFewMax = 32;  // requests of more rows are the many-rows kernel's
-
-struct Launches {
-    struct One {
-        int64_t tiles = 0;  // at most so many tiles (0: not launched)
-        int rows = 0, rows_lo = 0, rows_hi = 0;
-        int parts = 0, min_part = 1;
-        int64_t items = 0;
-        size_t slots(int64_t kv_heads) const { return parts ? (size_t)(items * kv_heads * rows) : 0; }
-        // Cut into about `want` parts of at least `least` tiles of `tile` keys.
-        void cut(int64_t want, int least, int64_t table_keys, int tile) {
-            min_part = least;
-            const int64_t most = (table_keys + (int64_t)tile * least - 1) / ((int64_t)tile * least);  // parts of a tile
-            if (tiles && most > 1 && want > 0) parts = (int)want;
-            items = parts ? (tiles + parts < tiles * most ? tiles + parts : tiles * most) : tiles;
-        }
-    } few, many;
-    int few_waves = 4;
-};
-
-Launches plan_launches(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
-                       int64_t requests, int64_t max_new) {
-    Launches p;
-    const int64_t group = heads / kv_heads, rows = tokens * group, cus = device_cu_count();
-    const int64_t holders = requests + 1 < tokens ? requests + 1 : tokens;  // requests with rows
-    if (max_new <= kFewMax / group || rows <= kFewMax) {
-        p.few.tiles = holders + rows / kFewRows;
-        p.few.rows_hi = 0x7fffffff;
-    } else {
-        // Of up to 4 requests with a chunk among them, the others may as well run with the chunks (one row
-        // in a tile of 128, its keys cut into parts like theirs): looking for them in a kernel of their
-        // own, and for their parts in a join, took 5 us where there were none.
-        if (requests > 4) {
-            p.few.tiles = kFewMax / kFewRows * holders;
-            p.few.rows_hi = kFewMax;
-            p.many.rows_lo = kFewMax;
-        }
-        const int64_t large = rows / (kFewMax + 1) + 1;
-        p.many.tiles = rows / kManyRows + (holders < large ? holders : large);
-        p.many.rows_hi = 0x7fffffff;
-    }
-    p.few.rows = kFewRows;
-    p.many.rows = kManyRows;
-    // Few rows. A CU takes some 35 GB/s of keys and values whatever its waves (8 waves over 777 keys of 8
-    // heads: 16 us), so only up to 256 keys (a tile a wave) does one workgroup of 8 waves take them all,
-    // with nothing to join; beyond, 4 waves a workgroup and twice as many parts as workgroups fit the
-    // chip, so that uneven ends are short (two rows over 120001 keys: 126 us, 152 with once as many).
-    if (table_keys <= 256 && !p.many.tiles) p.few_waves = 8;
-    // Beside the many-rows kernel's workgroups, which fill the chip, once is enough (two chunks and 31
-    // decoding requests: 45.0 -> 42.4 us).
-    const int64_t slots = (cus * 2 + kv_heads - 1) / kv_heads;  // workgroups that run at once, of a cache head
-    // Many requests over long tables end unevenly: three times the slots (64 requests of up to 8192 keys: 209
-    // -> 203 us, 128 of them 443 -> 439); over short tables the joins cost more (64 of up to 1500: 57 -> 60).
-    const int64_t times = p.many.tiles ? 1 : p.few.tiles > slots / 2 && table_keys >= 4096 ? 3 : 2;
-    p.few.cut(p.few_waves == 8 ? 0 : times * slots, 4, table_keys, 32);
-    // Many rows: cut only where whole tiles would leave slots empty, into as many parts as there are slots:
-    // twice as many cost more in partial sums (512 tokens over 32768: 38 MB) than even ends gain (322
-    // against 309 us; over short caches 27.6 against 28.1).
-    const int tile = head_dim > 128 ? kManyKeys<256> : kManyKeys<128>;
-    p.many.cut(p.many.tiles < slots ? slots : 0, 512 / tile, table_keys, tile);
-    return p;
+        join_rows<F16, DP, kFewRows, kFewKeys, RP>(a, few, (int)blockIdx.x - many_blocks, so, weight);
 }
 
 template <bool F16, int DP, bool FULL>
@@ -1107,7 +1039,8 @@ bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0;
 
 size_t paged_attention_workspace(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t table_keys,
                                  int64_t requests, int64_t max_new) {
-    const Launches p = plan_launches(tokens, heads, kv_heads, head_dim, table_keys, requests, max_new);
+    const Launches p = plan_launches(tokens, heads, kv_heads, head_dim, table_keys, requests, max_new,
+                                     device_cu_count());
     return (p.few.slots(kv_heads) + p.many.slots(kv_heads)) * (size_t)(4 * head_dim + 8);
 }
 
@@ -1124,7 +1057,8 @@ hipError_t launch_paged_attention(const AttnArgs& a, bool f16, int64_t max_new, 
         else attn_scalar_kernel<false><<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_keys, a.requests, max_new);
+    const Launches p = plan_launches(a.tokens, a.heads, a.kv_heads, a.dim, a.table_keys, a.requests, max_new,
+                                     device_cu_count());
     if (!grid_fits((p.few.items + p.many.items) * a.kv_heads, 512) || !grid_fits((p.few.tiles + p.many.tiles) * a.kv_heads, 256))
         return hipErrorInvalidConfiguration;
     if (a.dim <= 64) return f16 ? launch_dim<true, 64>(a, p, stream) : launch_dim<false, 64>(a, p, stream);
