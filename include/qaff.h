@@ -445,10 +445,11 @@ qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_d
  * and values): out[t, h] = sum_j p_j V[j], p = softmax_j(scale q[t, h] . K[j]) over the keys j that
  * t sees, with the keys and values of cache head h / (heads / kv_heads).
  *   Request b's new tokens are rows cu_new[b] .. cu_new[b + 1] - 1, the last of them at position
- *   kv_lens[b] - 1. A token at position p sees the keys j < kv_lens[b], of these with causal j <= p,
- *   and with window > 0 j > p - window. A token that sees no key gets zeros (and lse -infinity); so
- *   does a row past cu_new[requests]. Values and keys that a token does not see do not enter its row,
- *   whatever they hold.
+ *   kv_lens[b] - 1. Where cu_new goes past `tokens`, as after a plan for fewer rows than the step's
+ *   tokens, only the rows below `tokens` are there. A token at position p sees the keys
+ *   j < kv_lens[b], of these with causal j <= p, and with window > 0 j > p - window. A token that sees
+ *   no key gets zeros (and lse -infinity); so does a row past cu_new[requests]. Values and keys that a
+ *   token does not see do not enter its row, whatever they hold.
  *   q [tokens, heads, head_dim] with token and head strides in elements (the last axis contiguous);
  *   block_tables int32 [requests, table_width]; cu_new int32 [requests + 1], from 0 on and not
  *   decreasing; kv_lens int32 [requests]; out [tokens, heads, head_dim] contiguous; lse float32 [tokens, heads] or null: the

@@ -149,8 +149,8 @@ struct Sched {
 struct Item {
     int tile, part, parts;
     int first;       // the item of part 0
-    int row_end;     // rows of the request
-    int start, end;  // its rows of q, as cu gives them
+    int row_end;     // rows of the request that the call has
+    int start, end;  // its tokens, as cu gives them: the last is the one at position kv - 1
     int kv;
     int b;
 };
@@ -172,8 +172,9 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
             kv = a.kv_lens[b];
         }
         kv = max(kv, 0);
-        if (start >= 0 && end > start && end <= a.tokens) {
-            const int rows = (end - start) * a.group;  // at most tokens * heads < 2^31
+        // rows past the call's are not there, also of a request that begins before them
+        if (start >= 0 && start < min(end, a.tokens)) {
+            const int rows = (min(end, a.tokens) - start) * a.group;  // at most tokens * heads < 2^31
             tiles = tiles_of(rows, ROWS, s.rows_lo, s.rows_hi);
         }
         span = span_of(kv, a.window, a.table_keys, a.group, ROWS, KT);
@@ -216,7 +217,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int
             it.start = lane_value(start, at);
             it.end = lane_value(end, at);
             it.kv = lane_value(kv, at);
-            it.row_end = (it.end - it.start) * a.group;
+            it.row_end = (min(it.end, a.tokens) - it.start) * a.group;
             it.b = b0 + at;
             return true;
         }

@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import paged_ref as ref
 from gpu_util import banner
 from quantized_matmul_mlx_amd import _lib
 from test_gpu_paged import BF, HF, Case, ints
@@ -47,3 +48,30 @@ def test_few_requests_of_few_rows(new, heads, kv_heads, padding, exact, keys):
     c = Case([(keys + 3 * b, n) for b, n in enumerate(new)], heads, kv_heads, 64, 16, BF, pad_rows=padding)
     rows = c.q.shape[0]
     c.check(attend(c, rows, max(new) if exact else rows))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 20])
+@pytest.mark.parametrize("new", [[1] * 12, [20, 90, 70], [200], [3, 1, 150, 1, 1, 80, 1]], ids=str)
+@pytest.mark.parametrize("cut", [1, 2, 25])
+def test_fewer_rows_than_the_requests_tokens(dim, new, cut):
+    # cu_new says where the requests' tokens are, as a plan for fewer rows leaves it: the rows that are
+    # there come out as they do among all of them
+    banner(f"rows dim {dim} new {new} cut {cut}")
+    c = Case([(n + 37 * (b % 4), n) for b, n in enumerate(new)], 4, 2, dim, 16, HF)
+    rows = max(1, c.q.shape[0] - cut)
+    want, wlse, tol, ltol = (x[:rows] for x in ref.attention(c.q, c.k, c.v, c.tables, c.cu, c.kv, c.scale))
+    for max_new in (max(new), rows):
+        out, lse = (x.cpu().double() for x in attend(c, rows, max_new))
+        assert ((out - want).abs() <= tol).all()
+        assert ((lse - wlse).abs() <= ltol).all()
+
+
+def test_fewer_rows_over_a_cut_table():
+    # the same where the keys are cut into parts
+    c = Case([(2500, 1), (900, 60)], 4, 2, 128, 16, BF)
+    rows = 30
+    want, wlse, tol, ltol = (x[:rows] for x in ref.attention(c.q, c.k, c.v, c.tables, c.cu, c.kv, c.scale))
+    for max_new in (60, rows):
+        out, lse = (x.cpu().double() for x in attend(c, rows, max_new))
+        assert ((out - want).abs() <= tol).all()
+        assert ((lse - wlse).abs() <= ltol).all()
