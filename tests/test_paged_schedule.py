@@ -14,7 +14,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
                     reason="g++ or the HIP headers not available")
 def test_launches_hold_the_work_of_every_call(tmp_path):
     exe = tmp_path / "paged_sched"
-    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+    r = subprocess.run(["g++", "-std=c++17", "-O2", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
                         "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
                         "-I" + os.path.join(ROOT, "quantized_matmul_mlx_amd", "csrc"), "-o", str(exe),
                         os.path.join(ROOT, "tests", "sanitize", "paged_sched_driver.cpp")],
