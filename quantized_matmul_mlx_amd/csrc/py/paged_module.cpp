@@ -113,9 +113,14 @@ Caches caches(PyObject* ko, PyObject* vo, const at::Tensor& q) {
     if (k.sizes() != v.sizes())
         raise(PyExc_ValueError, "k_cache " + shape_of(k) + " and v_cache " + shape_of(v) + " differ");
     Caches c{k, v, k.size(0), k.size(1), k.size(2), k.size(3), k.stride(0)};
-    if (k.numel() && (k.stride(1) != c.page_size * c.dim || k.stride(2) != c.dim || k.stride(3) != 1))
-        raise(PyExc_ValueError, "each page of the caches must be contiguous: [kv_heads, page_size, head_dim]");
-    if (k.strides() != v.strides()) raise(PyExc_ValueError, "k_cache and v_cache differ in their strides");
+    // an axis of size 1 may have any stride
+    auto stride_is = [](const at::Tensor& t, int64_t axis, int64_t stride) {
+        return t.size(axis) <= 1 || t.stride(axis) == stride;
+    };
+    for (const at::Tensor* t : {&k, &v})
+        if (t->numel() && !(stride_is(*t, 1, c.page_size * c.dim) && stride_is(*t, 2, c.dim) && stride_is(*t, 3, 1)))
+            raise(PyExc_ValueError, "each page of the caches must be contiguous: [kv_heads, page_size, head_dim]");
+    if (k.numel() && !stride_is(v, 0, c.stride)) raise(PyExc_ValueError, "k_cache and v_cache differ in their strides");
     if (c.pages <= 1) c.stride = c.kv_heads * c.page_size * c.dim;
     return c;
 }
