@@ -428,8 +428,8 @@ qaff_status qaff_paged_plan(const int32_t* cached_lens, const int32_t* new_lens,
  * Float32 arithmetic, rounded to nearest even once at the end.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, odd rot, rot above head_dim, axes
  * outside 1 to 4, sections that do not fit, negative strides, null or misaligned pointers;
- * UNSUPPORTED for a page size not listed above, head_dim above 512, 2^31 tokens or more, or more
- * tokens than one launch holds (2^24).
+ * UNSUPPORTED for a page size not listed above, head_dim above 512, 2^31 tokens or pages or more, 2^20
+ * heads or more, or more tokens than one launch holds (2^24).
  */
 qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_dtype dtype, int64_t tokens,
                              int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t q_token_stride,
@@ -466,9 +466,9 @@ qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_d
  * for their product with V, whose sums are float32; out is rounded once at the end.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, heads not a multiple of kv_heads, a
  * scale that is not positive and finite, null or misaligned pointers, a short workspace; UNSUPPORTED
- * for a page size not listed above, head_dim above 256, more than 65536 requests, tokens * heads of
- * 2^31 or more, more rows than one launch holds (2^26 for head sizes and alignments without 16-byte
- * pieces), or a table of 2^30 tokens or more a request.
+ * for a page size not listed above, head_dim above 256, more than 65536 requests, 2^31 pages or cache
+ * heads or more, tokens * heads of 2^31 or more, more rows than one launch holds (2^26 for head sizes
+ * and alignments without 16-byte pieces), or a table of 2^30 tokens or more a request.
  */
 qaff_status qaff_paged_attention(const void* q, qaff_dtype dtype, int64_t tokens, int64_t heads,
                                  int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,

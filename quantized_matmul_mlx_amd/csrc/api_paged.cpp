@@ -62,6 +62,7 @@ qaff_status check_cache(const char* op, int64_t pages, int64_t page_stride, int6
                         int32_t page_size) {
     if (pages < 0 || page_stride < 0) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: negative cache size", op);
     if (pages >= k2G) return fail(QAFF_ERR_UNSUPPORTED, "%s: 2^31 pages or more", op);
+    if (kv_heads >= k2G) return fail(QAFF_ERR_UNSUPPORTED, "%s: 2^31 cache heads or more", op);
     if (pages > 1 && page_stride < kv_heads * head_dim * page_size)
         return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: pages %lld elements apart overlap", op, (long long)page_stride);
     return QAFF_OK;
