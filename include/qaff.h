@@ -455,7 +455,9 @@ qaff_status qaff_rope_append(const void* q, const void* k, const void* v, qaff_d
  *   decreasing; kv_lens int32 [requests]; out [tokens, heads, head_dim] contiguous; lse float32 [tokens, heads] or null: the
  *   natural logarithm of the sum of exponentials of the scaled scores.
  *   max_new: the largest number of new tokens of any request, or any bound of it: a hint for the
- *   choice of kernel. scale > 0.
+ *   choice of kernel. scale > 0. The time of a call has a part that grows with the square of the
+ *   requests (every workgroup looks through all of them): above a few thousand, several calls of some
+ *   of the requests each take less.
  *   A page outside the pool, or past the table, that a request's keys need is never read: rows that
  *   meet it come out as NaN.
  *   workspace: a device buffer of at least qaff_paged_attention_workspace_size(...) bytes, 16-byte

@@ -158,7 +158,10 @@ struct Item {
 
 // Item `want` (or the item of part 0 of tile `want`) of those that the schedule's requests make.
 // Every wave scans the requests itself, 64 at a time: with up to 64 requests that is one load of
-// each length and two scans, less than reading another kernel's schedule would cost.
+// each length and two scans, less than reading another kernel's schedule would cost. The scans of all
+// workgroups together grow with the square of the requests: decoding over up to 500 keys a request, 256
+// requests take 86 us, 1021 take 472 (38% more than four times as long), 4096 take 4.4 ms (three times
+// sixteen times as long); over up to 4000 keys they do not show up to 1021 requests.
 template <int ROWS, int KT>
 __device__ __forceinline__ bool find_item(const AttnArgs& a, const Sched& s, int want, bool by_tile, Item& it) {
     const int lane = threadIdx.x & 63;
@@ -368,7 +371,9 @@ __device__ __forceinline__ void softmax_tile(typename Shape<R>::acc (&sc)[SB], t
         }
 }
 
-// Eight probabilities rounded to 16 bits for their product with V (their sum l is taken before).
+// Eight probabilities rounded to 16 bits, as the matrix instructions take them, for their product with V:
+// half a step of the type each (2^-8 of it in bf16, 2^-11 in float16), while their sum l is taken before.
+// The error of the output is 1.2 to 1.4 times what its own rounding at the end alone makes.
 template <bool F16, typename V0, typename V1>
 __device__ __forceinline__ op8<F16> pack8(V0 a, V1 b) {
     return __builtin_bit_cast(op8<F16>, u32x4a{pack_half2<F16>(a[0], a[1]), pack_half2<F16>(a[2], a[3]),
@@ -425,8 +430,9 @@ __device__ void take_rows_again(const AttnArgs& a, const Sched& s, const Item& i
 // barrier in the loop. K is read from memory as the product wants it: 16 rows of 64 bytes an
 // instruction, a lane's 2 rows the same for K and V, so a tile costs it 2 table lookups and 2
 // addresses. A tile's keys are used before its values: their registers take the next tile's loads
-// at once, so a wave has about a tile (16 KB at 128 values) in flight all the time. Memory bounds it: 64
-// decoding requests of up to 8192 keys take 203 us with the join, 5.34 TB/s (a large copy: 5.0).
+// at once, so a wave has about a tile (16 KB at 128 values) in flight all the time. 64 decoding requests
+// of up to 8192 keys take 203 us with the join, 5.34 TB/s: three quarters of what a plain read of 1 GiB
+// reaches (7.1 TB/s); the counters show no busy unit, the waves wait for memory or to issue.
 template <int DP, int NS> constexpr int kFewLds = NS * (32 * DP * 2 + kFewRows * 8);
 template <bool F16, int DP, int NS, bool FULL>
 __device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int block, uint8_t* lds) {
@@ -632,10 +638,11 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Sched& s, int 
 }
 
 // Chunks and prompts: 4 waves of 32 rows. K and V tiles go through registers into LDS one tile ahead,
-// one barrier a tile. A prompt of 8192 (32 heads of 128): 562 to 585 us, 940 to 977 TFLOP/s; the matrix
-// cores are busy 44% of the time and the vector units 47%, which bounds it: the softmax, the tiles'
-// addresses and LDS accesses take as many issue slots as the products take cycles. Interleaving the
-// products with another tile's softmax within a wave, and loads straight into LDS, gave the same time.
+// one barrier a tile. A prompt of 8192 (32 heads of 128): 579 to 611 us, 900 to 949 TFLOP/s; the matrix
+// cores are busy 46% of a CU's time and the vector units 52%, one after the other for the most part: the
+// softmax, the tiles' addresses and LDS accesses take as many issue slots as the products take cycles.
+// Interleaving the products with another tile's softmax within a wave, and loads straight into LDS, gave
+// the same time.
 constexpr int kManyWaves = kManyRows / 32;
 template <int DP> constexpr int kManyKeys = many_keys(DP);
 template <int DP> constexpr int kManyLds = 2 * 2 * kManyKeys<DP> * DP * 2;  // two buffers of K and V

@@ -4,7 +4,7 @@
 // before b in the free list. The work is a few bytes a token; a launch bounds it. So there is one
 // launch: every workgroup scans all requests itself (two int32 arrays in LDS, 8 bytes a request)
 // instead of waiting for another kernel's scan, then each thread finds one token's request by a
-// binary search in LDS. 64 requests of one token: 2.7 us; 1021 requests with 49 K tokens: 5.2 us.
+// binary search in LDS. 64 requests of one token: 2.8 us; 1021 requests with 49 K tokens: 5.5 us.
 #include "paged.h"
 #include "wave.h"
 

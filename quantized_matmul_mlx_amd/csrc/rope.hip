@@ -11,10 +11,11 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-// Sine and cosine of pos * f. The product is exact in float64 (31 + 24 bits fit only nearly: 53),
-// and so is its reduction to a fraction of a turn, up to that rounding: at 2^20 positions a float32
-// angle would already be off by 2^-4 rad. The remaining fraction, at most half a turn, needs no more
-// than float32.
+// Sine and cosine of pos * f. The product (up to 31 + 24 bits of 53) and its scaling to turns each round
+// once in float64: together they are off by less than 2^-52 |turns| of a turn, which is nothing beside
+// the fraction's float32 rounding up to about 2^24 turns and as large as that at 2^28. At 2^20 positions
+// a float32 angle would already be off by 2^-4 rad. The remaining fraction, at most half a turn, needs no
+// more than float32.
 __device__ __forceinline__ float2 angle_of(int32_t pos, float f) {
     const double turns = (double)pos * (double)f * 0.15915494309189533577;  // 1 / (2 pi)
     const float r = (float)(turns - __builtin_rint(turns));
@@ -81,8 +82,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_scalar_kernel(RopeArgs a, i
 // 16 bytes at a time. A thread's unit is a piece of 8 values, or the two pieces whose values turn
 // together (values i and i + half). The loads do not wait for the angles: every thread first asks for
 // its units, then the workgroup computes the token's angles, then the units turn and go out. 8192 tokens
-// of 32 + 8 + 8 heads of 128: 41.6 us, 4.83 TB/s, a large copy's rate; two units a thread keep enough
-// loads on their way, one starts sooner where there are few (64 tokens: 3.0 us).
+// of 32 + 8 + 8 heads of 128: 41.7 us, 4.83 TB/s (a large copy: 4.8 to 5.2); two units a thread keep
+// enough loads on their way, one starts sooner where there are few (64 tokens: 3.5 us). A token of few heads
+// leaves most of its workgroup idle: 8192 tokens of 1 + 1 + 1 heads of 64 take 10.8 us for their 6.4 MB.
 template <bool F16, bool TRADITIONAL, int UNITS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int blocks_per_token) {
     __shared__ float2 turn[256];
