@@ -486,6 +486,98 @@ size_t qaff_paged_attention_workspace_size(int64_t tokens, int64_t heads, int64_
                                            int32_t page_size, int64_t table_width, int64_t requests,
                                            int64_t max_new);
 
+/*
+ * A decoder's feed-forward: the router of a mixture of experts, the layer of its experts, and products in
+ * 8-bit floating point (e4m3: 4 exponent and 3 mantissa bits, largest value 448, no infinities) with a
+ * float32 scale for each block of 128.
+ *
+ * qaff_moe_route: the top_k experts of each token and their weights.
+ *   logits [tokens, experts] of dtype (float32, bf16 or float16), rows row_stride elements apart; bias
+ *   float32 [experts] or null. score = softmax(logits), or 1 / (1 + exp(-logit)) where sigmoid is
+ *   non-zero. The experts of the largest keys are chosen, in falling order, of equal keys the lowest index
+ *   first: key = logit without a bias (exact: both scores grow with the logit), score + bias in float64
+ *   with one. weight = the score (without the bias), divided by the sum of the chosen scores where
+ *   renormalize is non-zero (0 if that sum is 0), times scale.
+ *   A NaN counts as -infinity; an expert of logit (or key) -infinity is chosen only where no other is left,
+ *   one of logit -infinity has weight 0. weights float32, chosen int32 [tokens, top_k].
+ * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, top_k above experts, a scale that is not
+ * finite, null or misaligned pointers; UNSUPPORTED for more than 1024 experts, top_k above 64, 2^26 tokens
+ * or more, or rows 2^32 elements apart or more.
+ */
+qaff_status qaff_moe_route(const void* logits, qaff_dtype dtype, int64_t tokens, int64_t experts,
+                           int64_t row_stride, const float* bias, int32_t sigmoid, int64_t top_k,
+                           int32_t renormalize, float scale, float* weights, int32_t* chosen,
+                           hipStream_t stream);
+
+/*
+ * The layer of a mixture of experts:
+ *   y[t] = resid[t] + sum_j weights[t, j] D[e] (silu(G[e] x[t]) * (U[e] x[t])),  e = chosen[t, j],
+ * over 0 <= j < top_k with 0 <= e < experts (other entries of chosen add nothing: experts on another GPU, padded
+ * tokens), silu(v) = v / (1 + exp(-v)).
+ *   x, y [tokens, width] and resid [tokens, width] or null, of dtype (bf16 or float16); chosen int32 and
+ *   weights float32 [tokens, top_k]; an expert may be named more than once by a token.
+ *   G (gate) and U (up) [experts, hidden, width] and D (down) [experts, width, hidden] in the storage format
+ *   above, all experts of a weight one after another, scales and biases of dtype; width and hidden are
+ *   multiples of group_size.
+ *   workspace: a device buffer of at least qaff_moe_ffn_workspace_size(...) bytes, 16-byte aligned, which
+ *   the call overwrites. y may be resid.
+ * Sums are float32, silu(g) * u is rounded to dtype for its product with D, y is rounded once at the end.
+ * Results are deterministic.
+ * Errors: INVALID_ARGUMENT for negative sizes, a dtype other than bf16 and float16, a bad group size, width
+ * or hidden that is not a multiple of it, null or misaligned pointers (2 bytes; 4 for codes, chosen and
+ * weights), a short workspace; UNSUPPORTED for a bit width not listed above, width or hidden above 32768,
+ * more than 65535 experts, 2^31 pairs (tokens * top_k) or more, 2^34 outputs or more.
+ */
+qaff_status qaff_moe_ffn(const void* x, qaff_dtype dtype, int64_t tokens, int64_t width, int64_t hidden,
+                         const int32_t* chosen, const float* weights, int64_t top_k, int64_t experts,
+                         const uint32_t* gate_packed, const void* gate_scales, const void* gate_biases,
+                         const uint32_t* up_packed, const void* up_scales, const void* up_biases,
+                         const uint32_t* down_packed, const void* down_scales, const void* down_biases,
+                         int32_t group_size, int32_t bits, const void* resid, void* workspace,
+                         size_t workspace_bytes, void* y, hipStream_t stream);
+
+/* Bytes of workspace qaff_moe_ffn needs for these sizes (0: none, or sizes that it refuses). */
+size_t qaff_moe_ffn_workspace_size(int64_t tokens, int64_t width, int64_t hidden, int64_t top_k,
+                                   int64_t experts, int32_t group_size, int32_t bits);
+
+/*
+ * Quantization to 8-bit floating point with a scale for each block of 128 columns of a row
+ * (block_rows 1: activations) or of 128 x 128 values (block_rows 128: weights); the last blocks of a row
+ * and of the rows may be smaller.
+ *   x [rows, cols] of dtype (float32, bf16 or float16), rows row_stride elements apart;
+ *   codes uint8 [rows, cols], e4m3; scales float32 [rows, ceil(cols / 128)], or
+ *   [ceil(rows / 128), ceil(cols / 128)].
+ *   scale = largest |x| of the block / 448; code = the e4m3 value nearest to x / scale, of two the even
+ *   one; both quotients are float32, rounded to nearest even. A scale of 0 gives codes 0. A block with a NaN or
+ *   an infinity has a scale that is NaN or infinite: its products are NaN.
+ * Errors: INVALID_ARGUMENT for negative sizes, an unknown dtype, block_rows other than 1 and 128, rows that
+ * overlap, null or misaligned pointers (x its element size, scales 4); UNSUPPORTED for 2^28 blocks of one
+ * row or more, or sizes that leave 32 bits.
+ */
+qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, int64_t cols,
+                                int64_t row_stride, int32_t block_rows, uint8_t* codes, float* scales,
+                                hipStream_t stream);
+
+/*
+ * The product of such operands, y = x . w^T:
+ *   y[m, n] = sum_j x_scales[m, j] w_scales[n / 128, j] sum_{128 j <= i < 128 (j + 1)} x[m, i] w[n, i]
+ *   x uint8 [m, k], x_scales float32 [m, ceil(k / 128)]; w uint8 [n, k], w_scales float32
+ *   [ceil(n / 128), ceil(k / 128)]; y [m, n] of y_dtype (float32, bf16 or float16).
+ * Sums are float32, y is rounded once at the end. k == 0 writes zeros. Rows of x and w that are 16-byte
+ * aligned (k a multiple of 16) take the fast kernels.
+ *   workspace: a device buffer of at least qaff_block_qmm_workspace_size(m, n, k) bytes, 16-byte aligned,
+ *   which the call overwrites (float32 partial sums where few rows split K, joined in a fixed order); may be
+ *   null where that size is 0. Results are deterministic.
+ * Errors: INVALID_ARGUMENT for negative sizes, an unknown y_dtype, null or misaligned pointers (scales 4
+ * bytes, y its element size), a short workspace; UNSUPPORTED for m or k of 2^31 or more, n of 2^28 or more.
+ */
+qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, const uint8_t* w,
+                           const float* w_scales, int64_t n, int64_t k, void* workspace,
+                           size_t workspace_bytes, void* y, qaff_dtype y_dtype, hipStream_t stream);
+
+/* Bytes of workspace qaff_block_qmm needs for these sizes (0: none). */
+size_t qaff_block_qmm_workspace_size(int64_t m, int64_t n, int64_t k);
+
 /* Text for the last non-OK status returned on the calling thread ("" if none). The pointer stays
  * valid until the thread's next qaff call. */
 const char* qaff_last_error(void);

@@ -23,6 +23,13 @@ Between the projections of a decoder layer, a serving step over a paged cache (`
     plan = paged_plan(cached_lens, new_lens, free_pages, block_tables, page_size, tokens)
     q = rope_append(q, k, v, plan.positions, inv_freq, plan.slots, k_cache, v_cache)
     o = paged_attention(q, k_cache, v_cache, block_tables, plan.cu_new, plan.kv_lens)
+
+A mixture of experts, and 8-bit floating point with a scale for each block of 128 (``ffn``):
+
+    weights, experts = moe_route(router_logits, top_k)
+    y = moe_ffn(x, experts, weights, gate, up, down, group_size, bits, resid=r)
+    codes, scales = block_quantize(x)
+    y = block_qmm(codes, scales, w_codes, w_scales)
 """
 from __future__ import annotations
 
@@ -33,10 +40,12 @@ import torch
 
 from . import _lib
 from ._lib import QaffError
+from .ffn import BlockWeight, block_qmm, block_quantize, moe_ffn, moe_route
 from .paged import PagedPlan, paged_attention, paged_plan, rope_append
 
 __all__ = ["quantize", "dequantize", "qmm", "qmm_nt", "dequant_rows", "gemv_gate_up", "gemv_silu_gate", "gather_qmm", "QWeight",
-           "QaffError", "gemv_max_m", "gemv_mfma_min_m", "PagedPlan", "paged_plan", "rope_append", "paged_attention"]
+           "QaffError", "gemv_max_m", "gemv_mfma_min_m", "PagedPlan", "paged_plan", "rope_append", "paged_attention",
+           "moe_route", "moe_ffn", "block_quantize", "block_qmm", "BlockWeight"]
 
 _PACKED_DTYPES = (torch.int32, torch.uint32)
 _BF16_BITS_DTYPES = (torch.bfloat16, torch.int16, torch.uint16)

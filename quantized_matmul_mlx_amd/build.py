@@ -1,11 +1,12 @@
 """Builds libqaff.so (HIP, gfx950 only) in-tree with hipcc, and beside it libqaff_bench.so (the
-benchmark's measurement aids, include/qaff_bench.h; not linked into libqaff.so) and _paged.so (the
-binding of the paged-cache operators, a CPython module on torch's C++ tensors that calls libqaff.so).
+benchmark's measurement aids, include/qaff_bench.h; not linked into libqaff.so) and _paged.so and
+_ffn.so (the bindings of the paged-cache and the feed-forward operators, CPython modules on torch's C++
+tensors that call libqaff.so).
 
     python -m quantized_matmul_mlx_amd.build          # or __graft_entry__.build()
 
 Each source compiles to an object under _build/ in parallel, then they link into
-quantized_matmul_mlx_amd/libqaff.so, libqaff_bench.so and _paged.so. Always recompiles.
+quantized_matmul_mlx_amd/libqaff.so, libqaff_bench.so, _paged.so and _ffn.so. Always recompiles.
 """
 from __future__ import annotations
 
@@ -21,8 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqaff.so")
 BENCH_LIB = os.path.join(PKG, "libqaff_bench.so")
-MODULE = os.path.join(PKG, "_paged.so")
-MODULE_SOURCE = os.path.join("py", "paged_module.cpp")
+# CPython modules: name -> source
+MODULES = {"_paged": os.path.join("py", "paged_module.cpp"), "_ffn": os.path.join("py", "ffn_module.cpp")}
 
 # every .hip and .cpp file under csrc/ goes into libqaff.so, except the benchmark's aids
 BENCH_SOURCES = ["bench_aux.hip"]
@@ -65,30 +66,31 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
-def _compile_module(verbose: bool) -> str:
-    """The CPython module: host code only, with the host compiler against torch's headers."""
-    obj = os.path.join(BUILD, "paged_module.o")
+def _compile_module(name: str, verbose: bool) -> str:
+    """A CPython module: host code only, with the host compiler against torch's headers."""
+    obj = os.path.join(BUILD, name + ".o")
     inc = os.path.join(_torch_dir(), "include")
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__",
            "-DUSE_ROCM", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
            "/opt/rocm/include", "-I", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), "-c",
-           os.path.join(CSRC, MODULE_SOURCE), "-o", obj]
+           os.path.join(CSRC, MODULES[name]), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed on {MODULE_SOURCE}:\n{r.stdout}{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on {MODULES[name]}:\n{r.stdout}{r.stderr}")
     return obj
 
 
-def _link_module(obj: str, verbose: bool) -> None:
-    tmp = MODULE + ".tmp"
+def _link_module(name: str, obj: str, verbose: bool) -> None:
+    lib = os.path.join(PKG, name + ".so")
+    tmp = lib + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libqaff.so", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, MODULE)
+    os.replace(tmp, lib)
 
 
 def _link(lib: str, objs, verbose: bool) -> None:
@@ -104,11 +106,12 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = SOURCES + BENCH_SOURCES
     with ThreadPoolExecutor(max_workers=min(len(srcs), 8)) as ex:
-        module = ex.submit(_compile_module, verbose)
+        modules = {name: ex.submit(_compile_module, name, verbose) for name in MODULES}
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
     _link(LIB, [objs[s] for s in SOURCES], verbose)
     _link(BENCH_LIB, [objs[s] for s in BENCH_SOURCES], verbose)
-    _link_module(module.result(), verbose)
+    for name, obj in modules.items():
+        _link_module(name, obj.result(), verbose)
     return LIB
 
 

@@ -1,48 +1,17 @@
 // The C ABI of the paged-cache operators (include/qaff.h): argument checks, all on the host before
 // any launch, and dispatch. Lengths, tables and slots live on the device and cannot be checked here:
 // the kernels bound every index that they take from them.
-#include "qaff.h"
-
+#include "api_util.h"
 #include "paged.h"
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <cstdlib>
-#include <cstring>
 
 namespace {
 
-qaff_status fail(qaff_status st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    qaff::set_error(buf);
-    return st;
-}
-
-qaff_status after_launch(const char* op, hipError_t e, hipStream_t stream) {
-    static const bool sync = [] {
-        const char* v = std::getenv("QAFF_DEBUG_SYNC");
-        return v && v[0] && std::strcmp(v, "0") != 0;
-    }();
-    if (e == hipErrorInvalidConfiguration)
-        return fail(QAFF_ERR_UNSUPPORTED, "%s: more rows than one launch holds (2^32 threads)", op);
-    if (e == hipSuccess && sync) e = hipStreamSynchronize(stream);
-    if (e != hipSuccess) return fail(QAFF_ERR_DEVICE, "%s: %s", op, hipGetErrorString(e));
-    return QAFF_OK;
-}
-
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// A pointer that a non-empty size needs: set and aligned.
-qaff_status check_ptr(const char* op, const char* name, const void* p, uintptr_t a) {
-    if (!p) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: null %s", op, name);
-    if (!aligned(p, a)) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: %s must be %d-byte aligned", op, name, (int)a);
-    return QAFF_OK;
-}
+using qaff::after_launch;
+using qaff::aligned;
+using qaff::check_ptr;
+using qaff::fail;
 
 // log2 of a supported page size, or -1.
 int page_shift_of(int32_t page_size) {

@@ -1,0 +1,164 @@
+// The router of a mixture of experts: for each token the top_k experts of the largest keys (ties to
+// the lowest index) and their weights.
+//
+//   key[e] = logit[e], or score[e] + bias[e] with a bias; score = softmax(logits) or 1 / (1 + exp(-logit))
+//   weight = score of the chosen expert (over the sum of the chosen ones' scores), times a factor
+//
+// Both scores grow with the logit, so without a bias the choice needs no score and is exact. With one,
+// the scores are float64: two sums that differ in the seventh digit still come in their order.
+//
+// A token takes 2^n lanes (16 lanes of 8 logits for 128 experts, a wave at most), so that a step of
+// the search for the largest key serves several tokens: in each lane over its own logits, then over the
+// lanes. The chosen key is struck out and the search repeats, top_k times.
+#include "ffn.h"
+#include "qaff_device.h"
+
+namespace qaff {
+namespace {
+
+// Lanes that hold one token's logits: lane i of the group has experts i, i + LANES, ...
+template <int LANES, typename T>
+__device__ __forceinline__ T group_max(T v) {
+#pragma unroll
+    for (int d = LANES / 2; d >= 1; d >>= 1) {
+        const T o = __shfl_xor(v, d, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ int group_min(int v) {
+#pragma unroll
+    for (int d = LANES / 2; d >= 1; d >>= 1) v = min(v, __shfl_xor(v, d, 64));
+    return v;
+}
+template <int LANES, typename T>
+__device__ __forceinline__ T group_sum(T v) {
+#pragma unroll
+    for (int d = LANES / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+template <typename K> struct Math;
+template <> struct Math<float> {
+    static __device__ __forceinline__ float exp(float v) { return ::expf(v); }
+};
+template <> struct Math<double> {
+    static __device__ __forceinline__ double exp(double v) { return ::exp(v); }
+};
+
+// K: the type of keys and scores (double where a bias takes part in the choice).
+template <int LANES, int EACH, typename K>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+    constexpr int kTokens = 256 / LANES;
+    const int lane = threadIdx.x % LANES;
+    const int64_t token = (int64_t)blockIdx.x * kTokens + threadIdx.x / LANES;
+    // a group past the last token repeats it: all lanes stay in the exchanges below
+    const int64_t t = token < a.tokens ? token : a.tokens - 1;
+    const K none = -__builtin_inf();
+    K x[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = lane + i * LANES;
+        x[i] = e < a.experts ? (K)load_as_f32(a.logits, (size_t)(t * a.row_stride + e), a.dtype) : none;
+        if (!(x[i] == x[i])) x[i] = none;  // a NaN is never better than a number
+    }
+    // softmax: the largest logit and the sum of exp(logit - largest); no expert left: sum 0
+    K top = none, sum = 0;
+    const bool softmax = !a.sigmoid;
+    if (softmax) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) top = x[i] > top ? x[i] : top;
+        top = group_max<LANES>(top);
+    }
+    auto score = [&](K v) -> K {  // softmax: before the division by the sum
+        if (v == none) return 0;
+        if (a.sigmoid) return 1 / (1 + Math<K>::exp(-v));
+        return v == top ? (K)1 : Math<K>::exp(v - top);
+    };
+    if (softmax && (a.bias || !a.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) sum += score(x[i]);
+        sum = group_sum<LANES>(sum);
+    }
+    K key[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        key[i] = x[i];
+        const int e = lane + i * LANES;
+        if (a.bias && x[i] != none) {
+            const K s = score(x[i]);
+            const K k = (softmax ? s / sum : s) + (K)a.bias[e];
+            key[i] = k == k ? k : none;
+        }
+    }
+    // top_k rounds; lane r of the group keeps the r-th chosen expert (r, r + LANES, ... where top_k is larger)
+    constexpr int kKeep = (kRouteMaxChosen + LANES - 1) / LANES;
+    int mine[kKeep];
+    K mine_x[kKeep];
+    uint32_t taken = 0;  // bit i: this lane's logit i is chosen already
+    K total = 0;
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        mine[j] = 0;
+        mine_x[j] = none;
+        for (int r = 0; r < LANES && j * LANES + r < a.top_k; ++r) {
+            K best = none;
+            int at = 1 << 30;
+            K at_x = none;
+#pragma unroll
+            for (int i = EACH - 1; i >= 0; --i) {  // from the back: of equal keys the lowest index stays
+                const int e = lane + i * LANES;
+                if (!(taken >> i & 1) && e < a.experts && key[i] >= best) {
+                    best = key[i];
+                    at = e;
+                    at_x = x[i];
+                }
+            }
+            const K most = group_max<LANES>(best);
+            const int who = group_min<LANES>(best == most ? at : 1 << 30);
+            if (who == at) taken |= 1u << (at / LANES);
+            at_x = __shfl(at_x, who % LANES, LANES);
+            if (lane == r) {
+                mine[j] = who;
+                mine_x[j] = at_x;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        mine_x[j] = j * LANES + lane < a.top_k ? score(mine_x[j]) : (K)0;
+        total += mine_x[j];
+    }
+    total = a.renormalize ? group_sum<LANES>(total) : softmax ? sum : (K)1;
+    if (token >= a.tokens) return;
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int r = j * LANES + lane;
+        if (r >= a.top_k) continue;
+        const K w = total > 0 ? mine_x[j] / total : (K)0;
+        a.chosen[token * a.top_k + r] = mine[j];
+        a.weights[token * a.top_k + r] = (float)(w * (K)a.scale);
+    }
+}
+
+template <int LANES, int EACH>
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+    constexpr int kTokens = 256 / LANES;
+    const unsigned blocks = (unsigned)((a.tokens + kTokens - 1) / kTokens);
+    if (a.bias) route_kernel<LANES, EACH, double><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+    else route_kernel<LANES, EACH, float><<<dim3(blocks), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
+    if (a.experts <= 64) return launch_route<16, 4>(a, stream);
+    if (a.experts <= 128) return launch_route<16, 8>(a, stream);
+    if (a.experts <= 256) return launch_route<32, 8>(a, stream);
+    if (a.experts <= 512) return launch_route<64, 8>(a, stream);
+    return launch_route<64, 16>(a, stream);
+}
+
+}  // namespace qaff
