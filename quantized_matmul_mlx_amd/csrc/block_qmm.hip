@@ -88,11 +88,239 @@ __global__ __launch_bounds__(64 * kWaves) void qmm_small_kernel(BlockQmmArgs a) 
         if (m0 + 4 * g + v < a.m) store_from_f32(a.y, (size_t)((m0 + 4 * g + v) * a.n + n0 + r), a.dtype, acc[v]);
 }
 
+// ---- tiles -----------------------------------------------------------------------------------------
+//
+// Many rows: a workgroup of 4 waves has 16 MT x 64 NT outputs, wave w the columns 16 NT w of them and all rows.
+//  * w goes straight from memory into the products' operands, three blocks of K ahead in registers: no
+//    wave shares its rows, and LDS, which the rows of x already fill, carries it not.
+//  * x goes through LDS, two blocks at a time (16-byte pieces, swapped within a row by half the row's
+//    number so that 16 rows at one offset fall on distinct banks), with the products of its and w's scales beside it.
+//  * One v_mfma_f32_16x16x128_f8f6f4 is a block of K for 16 x 16 outputs (32 cycles); its four results a
+//    lane enter the totals with the scales by four multiply-adds (16 cycles), those of the previous 16 rows
+//    while the products of these run.
+//  * EXACT: products of float16 operands instead, for float32 outputs (the others have 16 bits).
+// A lane's 32 values of a block are the pieces lane / 16 and 4 + lane / 16, of x and w alike.
+
+__device__ __forceinline__ f32x4 mfma_f8(i32x8 a, i32x8 b) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+template <int T> struct Type { static constexpr int value = T; };
+
+// TAIL: k is not a multiple of 128 (but of 16): the last block's pieces past the end are 0 in w.
+template <int WAVES, int MT, int NT, bool EXACT, bool TAIL>
+__global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, int tiles_m, int tiles_n) {
+    constexpr int kThreads = 64 * WAVES, kRows = 16 * MT, kCols = 16 * WAVES * NT;
+    constexpr int kPieces = kRows * 8 / kThreads;  // pieces of x a thread and block
+    constexpr int kScales = kCols / kBlock;        // blocks of 128 columns
+    constexpr int kPanel = kThreads / kRows;       // blocks of K whose scales are loaded together
+    constexpr int kStages = 3;
+    __shared__ __attribute__((aligned(16))) uint8_t xl[kStages][kRows * kBlock];
+    __shared__ __attribute__((aligned(16))) float sl[2][kPanel][kScales][kRows];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    const int64_t m0 = (int64_t)tm * kRows, n0 = (int64_t)tn * kCols;
+    const int kb = (int)((a.k + kBlock - 1) / kBlock);
+
+    // this thread's pieces of x: row and place in LDS; its scales: row tid % kRows, block tid / kRows of a panel
+    const uint8_t* xp[kPieces];
+    int slot[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int row = (i * kThreads + tid) / 8;
+        xp[i] = a.x + min(m0 + row, a.m - 1) * a.k;
+        slot[i] = row * kBlock + ((tid & 7) ^ (row >> 1 & 7)) * 16;
+    }
+    const int scale_row = tid % kRows, scale_block = tid / kRows;
+    const float* xsp = a.x_scales + min(m0 + scale_row, a.m - 1) * kb;
+    const uint8_t* wp[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) wp[j] = a.w + min(n0 + wave * 16 * NT + 16 * j + r16, a.n - 1) * a.k;
+
+    struct Ahead {
+        u32x4a x[kPieces];
+        u32x4a lo[NT], hi[NT];
+    };
+    struct Scales {
+        float x, w[kScales];
+    };
+    // Blocks past the last one repeat it (their scales are stored as 0).
+    auto load_x = [&](Ahead& s, int b) {
+        b = min(b, kb - 1);
+        const int left = TAIL ? (int)min(a.k - (int64_t)b * kBlock, (int64_t)kBlock) : kBlock;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)  // a piece past the row's end repeats the last one: w is 0 there
+            s.x[i] = *reinterpret_cast<const u32x4a*>(xp[i] + (int64_t)b * kBlock + min(16 * (tid & 7), left - 16));
+    };
+    auto load_w = [&](Ahead& s, int b) {
+        b = min(b, kb - 1);
+        const int left = TAIL ? (int)min(a.k - (int64_t)b * kBlock, (int64_t)kBlock) : kBlock;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            s.lo[j] = *reinterpret_cast<const u32x4a*>(wp[j] + (int64_t)b * kBlock + min(16 * g, left - 16));
+            s.hi[j] = *reinterpret_cast<const u32x4a*>(wp[j] + (int64_t)b * kBlock + min(64 + 16 * g, left - 16));
+        }
+    };
+    auto load_scales = [&](Scales& s, int panel) {
+        const int b = min(panel * kPanel + scale_block, kb - 1);
+        s.x = xsp[b];
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) s.w[i] = a.w_scales[min(n0 / kBlock + i, (a.n - 1) / kBlock) * kb + b];
+    };
+    auto store_scales = [&](const Scales& s, int panel) {
+#pragma unroll
+        for (int i = 0; i < kScales; ++i)
+            sl[panel & 1][scale_block][i][scale_row] = panel * kPanel + scale_block < kb ? s.x * s.w[i] : 0.f;
+    };
+    auto operand = [&](const Ahead& s, int j, int b) {
+        u32x4a lo = s.lo[j], hi = s.hi[j];
+        if constexpr (TAIL) {
+            const int64_t left = a.k - (int64_t)b * kBlock;
+            if (16 * g >= left) lo = u32x4a{0u, 0u, 0u, 0u};
+            if (64 + 16 * g >= left) hi = u32x4a{0u, 0u, 0u, 0u};
+        }
+        return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    auto store_x = [&](const Ahead& s, int stage) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<u32x4a*>(&xl[stage][slot[i]]) = s.x[i];
+    };
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // x operand and scales of 16 rows. Read one turn ahead, over the border of two blocks too.
+    const int p0 = r16 * kBlock + (g ^ (r16 >> 1)) * 16, p1 = r16 * kBlock + ((4 + g) ^ (r16 >> 1)) * 16;
+    const int sw = wave * 16 * NT / kBlock;
+    i32x8 x[2];
+    f32x4 scale[3], d[2][NT];
+    auto read = [&](int stage, int b, int i) {
+        const u32x4a lo = *reinterpret_cast<const u32x4a*>(&xl[stage][16 * i * kBlock + p0]);
+        const u32x4a hi = *reinterpret_cast<const u32x4a*>(&xl[stage][16 * i * kBlock + p1]);
+        x[i & 1] = i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    auto read_scale = [&](int b, int i, int to) {
+        scale[to] = *reinterpret_cast<const f32x4*>(&sl[b / kPanel & 1][b % kPanel][sw][16 * i + 4 * g]);
+    };
+    static_assert(MT % 2 == 0, "a block's first turn follows an odd one");
+    auto products = [&](const Ahead& s, int b, int stage) {
+        i32x8 w[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w[j] = operand(s, j, b);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if (i + 1 < MT) read(stage, b, i + 1);
+            else read((stage + 1) % kStages, b + 1, 0);
+            // each product is followed by the scaling of the same columns one turn before (16 rows above, or the
+            // last rows of the block before); the compiler would put the scaling first, where its operands are
+            // not there yet
+            f32x4 now = scale[0];
+            read_scale(i + 1 < MT ? b : b + 1, (i + 1) % MT, 0);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                d[i & 1][j] = EXACT ? block_sums(x[i & 1], w[j]) : mfma_f8(x[i & 1], w[j]);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x4& sum = acc[(i + MT - 1) % MT][j];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) sum[v] = __builtin_fmaf(scale[1][v], d[(i + 1) & 1][j][v], sum[v]);
+                asm volatile("" : "+v"(sum));  // here, not sunk past the branches below, with its operands kept alive
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            scale[1] = now;
+        }
+    };
+
+    Ahead s[3];
+    Scales sc;
+    load_scales(sc, 0);
+    load_x(s[0], 0);
+    load_x(s[1], 1);
+    load_w(s[0], 0);
+    store_scales(sc, 0);
+    load_scales(sc, 1);
+    store_x(s[0], 0);
+    store_x(s[1], 1);
+    load_x(s[2], 2);
+    load_w(s[1], 1);
+    load_x(s[0], 3);
+    load_w(s[2], 2);
+    load_x(s[1], 4);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) d[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    scale[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();
+    read(0, 0, 0);
+    read_scale(0, 0, 0);
+    for (int b = 0; b < kb; b += 3) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            // After this barrier nobody reads block b + i - 1 any more, whose place block b + i + 2 takes; block
+            // b + i + 1, stored one turn ago, is there.
+            __syncthreads();
+            store_x(s[(i + 2) % 3], (i + 2) % 3);
+            load_x(s[(i + 2) % 3], b + i + 5);
+            if ((b + i) % kPanel == 0) {  // the panel of the blocks b + i + kPanel ..
+                store_scales(sc, (b + i) / kPanel + 1);
+                load_scales(sc, (b + i) / kPanel + 2);
+            }
+            products(s[i], b + i, i);
+            load_w(s[i], b + i + 3);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[MT - 1][j][v] = __builtin_fmaf(scale[1][v], d[1][j][v], acc[MT - 1][j][v]);
+    auto store = [&](auto type) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t m = m0 + 16 * i + 4 * g + v;
+                if (m >= a.m) continue;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int64_t n = n0 + wave * 16 * NT + 16 * j + r16;
+                    if (n < a.n) store_from_f32(a.y, (size_t)(m * a.n + n), type.value, acc[i][j][v]);
+                }
+            }
+    };
+    if (EXACT) store(Type<0>());
+    else if (a.dtype == 1) store(Type<1>());
+    else store(Type<2>());
+}
+
+template <int WAVES, int MT, int NT>
+hipError_t launch_tiles(const BlockQmmArgs& a, hipStream_t stream) {
+    const int tiles_m = (int)((a.m + 16 * MT - 1) / (16 * MT));
+    const int tiles_n = (int)((a.n + 16 * WAVES * NT - 1) / (16 * WAVES * NT));
+    const dim3 grid((unsigned)tiles_m * (unsigned)tiles_n), block(64 * WAVES);
+    if (a.k % kBlock) {
+        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, true, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        else qmm_tile_kernel<WAVES, MT, NT, false, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+    } else {
+        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, true, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        else qmm_tile_kernel<WAVES, MT, NT, false, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t block_qmm_workspace(int64_t, int64_t, int64_t) { return 0; }
 
 hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t stream) {
+    const bool aligned = a.k > 0 && a.k % 16 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.w % 16 == 0;
+    if (aligned && a.m > 64 && a.m * a.n < (int64_t)1 << 40) {
+        const int64_t big = ((a.m + 127) / 128) * ((a.n + 255) / 256);
+        if (big >= device_cu_count() * 3 / 4) return launch_tiles<8, 8, 2>(a, stream);
+        return launch_tiles<4, 4, 2>(a, stream);
+    }
     const int64_t rows = 65535 * 16;  // a grid's second axis
     for (int64_t m0 = 0; m0 < a.m; m0 += rows) {
         BlockQmmArgs p = a;

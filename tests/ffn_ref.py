@@ -104,12 +104,17 @@ def quantize(x, block_rows=1):
     return q.reshape(nb * block_rows, -1)[:rows, :cols].contiguous().to(torch.float8_e4m3fn), scale
 
 
-def product(x, xs, w, ws, dtype):
-    """float64 y and its bound: float32 sums of at most 128 terms a block, scaled and added block by block."""
+def product(x, xs, w, ws, dtype, eights=False):
+    """float64 y and its bound: float32 sums of at most 128 terms a block, scaled and added block by block.
+    With `eights`, sums of the 8-bit matrix instructions: of each eight products, those beside the largest lose
+    less than 2^-13 of its power of two (seven of them)."""
     m, k = x.shape
     n = w.shape[0]
     a = x.double() * xs.double().repeat_interleave(128, 1)[:, :k]
     b = w.double() * ws.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
     y = a @ b.T
     err = (a.abs() @ b.abs().T) * (k / 128 + 128 + 4) * F32
+    if eights:
+        for at in range(0, k, 8):
+            err += 7 * 2.0 ** -13 * (a[:, None, at:at + 8] * b[None, :, at:at + 8]).abs().amax(-1)
     return y, err + HALF[dtype] * (y.abs() + err) + TINY[dtype]
