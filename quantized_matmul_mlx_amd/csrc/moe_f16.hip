@@ -1,5 +1,5 @@
-// The layer of a mixture of experts in float16 (moe_few_impl.h).
-#include "moe_few_impl.h"
+// The layer of a mixture of experts in float16 (moe_few_impl.h: few rows an expert, moe_gemm_impl.h: many).
+#include "moe_gemm_impl.h"
 
 namespace qaff {
 
