@@ -22,6 +22,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 namespace qaff {
 namespace {
 
@@ -30,8 +32,11 @@ typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32h __attribute__((aligned(2)));
 
 constexpr int kTileRows = 16;  // rows of x a pass
-constexpr int kUnit = 2;       // chunks of 128 codes that are loaded together
+// Chunks of 128 codes that are loaded together: two units of two weights are in registers at a time.
+template <int BITS> constexpr int kUnit = BITS <= 4 ? 2 : 1;
 constexpr int kFewWaves = 4;
+constexpr int kFewBlocks = 3;  // workgroups a compute unit (168 registers a lane)
+constexpr int kFewThreads = 64 * kFewWaves;
 
 struct FewArgs {
     const uint16_t* x;           // rows of k values
@@ -43,7 +48,6 @@ struct FewArgs {
     int k, kpad, n, top_k, experts;
     int rows;                    // rows of x in LDS (1 to 16)
     int ksplit;                  // waves that share a tile's K
-    int by_pair;                 // grid y walks pairs (the first of each expert works) instead of experts
 };
 
 // ---- codes as operands ----------------------------------------------------------------------------
@@ -52,13 +56,23 @@ struct FewArgs {
 // themselves. float16 holds 1024 + c.
 template <bool F16, int BITS> constexpr float kCodeBase = F16 ? 1024.f : BITS == 8 ? 0.f : 128.f;
 
+// The mask of two 4-bit codes in a scalar and B (both halves) in a vector register, for one v_and_or_b32 for two codes.
+struct CodeConsts {
+    uint32_t mask, base;
+};
+template <bool F16> __device__ __forceinline__ CodeConsts make_code_consts() {
+    uint32_t base = F16 ? 0x64006400u : 0x43004300u;
+    asm volatile("" : "+v"(base));
+    return CodeConsts{(uint32_t)__builtin_amdgcn_readfirstlane(0x000F000F), base};
+}
+
 template <bool F16, int BITS>
-__device__ __forceinline__ u32x4a code_operand(const uint32_t (&w)[BITS], int j) {
-    constexpr uint32_t base = F16 ? 0x64006400u : 0x43004300u;
+__device__ __forceinline__ u32x4a code_operand(const uint32_t (&w)[BITS], int j, const CodeConsts& cc) {
+    const uint32_t base = cc.base;
     u32x4a o;
     if constexpr (BITS == 4) {  // pairs (c0, c4), (c1, c5), (c2, c6), (c3, c7): x is staged in that order
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = ((w[j] >> (4 * e)) & 0x000F000Fu) | base;
+        for (int e = 0; e < 4; ++e) o[e] = ((w[j] >> (4 * e)) & cc.mask) | base;
     } else if constexpr (BITS == 8 && F16) {  // bytes of the word between bytes of the base
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -111,16 +125,16 @@ template <int GSHIFT> constexpr int x_step_offset(int i) {
 
 // The operands of one chunk, register i of lane group g as x_lane_offset + x_step_offset say.
 template <bool F16, int BITS, int GSHIFT>
-__device__ __forceinline__ void chunk_operands(const uint32_t (&w)[BITS], op8<F16> (&o)[4]) {
+__device__ __forceinline__ void chunk_operands(const uint32_t (&w)[BITS], const CodeConsts& cc, op8<F16> (&o)[4]) {
     if constexpr (BITS == 4) {  // an octet is a word: exchanged before it is spread
         uint32_t v[4] = {w[0], w[1], w[2], w[3]};
         regroup<GSHIFT>(v[0], v[1], v[2], v[3]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __builtin_bit_cast(op8<F16>, code_operand<F16, 4>(v, j));
+        for (int j = 0; j < 4; ++j) o[j] = __builtin_bit_cast(op8<F16>, code_operand<F16, 4>(v, j, cc));
     } else {
         u32x4a v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = code_operand<F16, BITS>(w, j);
+        for (int j = 0; j < 4; ++j) v[j] = code_operand<F16, BITS>(w, j, cc);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             uint32_t r0 = v[0][e], r1 = v[1][e], r2 = v[2][e], r3 = v[3][e];
@@ -134,12 +148,14 @@ __device__ __forceinline__ void chunk_operands(const uint32_t (&w)[BITS], op8<F1
 
 // ---- loads ------------------------------------------------------------------------------------------
 
-// A unit's codes, scales and biases of one weight row: kUnit blocks of this lane, and the unit's groups.
+// A unit's codes, scales and biases of one weight row: kUnit blocks of this lane, and the unit's groups, as many as
+// a whole unit has. `over`: groups that the window had to start early to stay inside the tensor.
 template <int BITS, int GSHIFT> struct UnitLoads {
-    static constexpr int kGroups = kUnit * 4 >> GSHIFT;
+    static constexpr int kGroups = kUnit<BITS> * 4 >> GSHIFT;
     static constexpr int kWords = (kGroups + 1) / 2;
-    uint32_t w[kUnit][BITS];
+    uint32_t w[kUnit<BITS>][BITS];
     uint32_t s[kWords], b[kWords];
+    int over;
 };
 
 template <int WORDS> __device__ __forceinline__ void load_halves(const uint16_t* p, uint32_t (&o)[WORDS]) {
@@ -154,133 +170,195 @@ template <int WORDS> __device__ __forceinline__ void load_halves(const uint16_t*
     }
 }
 
-// Unit u of weight row `row` (counted over all experts). Blocks past the row's end repeat its last one:
-// x is 0 there. Groups likewise.
+// Unit u of weight row `row` (counted over all experts, of `all` rows). The blocks past the row's end repeat its
+// last one (x is 0 there); the groups past it are the next row's, and are masked where they are used.
 template <int BITS, int GSHIFT>
-__device__ __forceinline__ void load_unit(UnitLoads<BITS, GSHIFT>& L, const ExpertWeight& W, int64_t row, int u, int kb,
-                                          int g) {
+__device__ __forceinline__ void load_unit(UnitLoads<BITS, GSHIFT>& L, const ExpertWeight& W, int64_t row, int64_t all, int u,
+                                          int kb, int g) {
     typedef UnitLoads<BITS, GSHIFT> U;
     const int gpr = kb >> GSHIFT;
-    const uint16_t* sp = W.scales + row * gpr;
-    const uint16_t* bp = W.biases + row * gpr;
-    if ((u + 1) * (4 * kUnit) <= kb) {
-        load_halves(sp + u * U::kGroups, L.s);
-        load_halves(bp + u * U::kGroups, L.b);
-    } else {
-#pragma unroll
-        for (int i = 0; i < U::kWords; ++i) {
-            const int g0 = min(u * U::kGroups + 2 * i, gpr - 1), g1 = min(u * U::kGroups + 2 * i + 1, gpr - 1);
-            L.s[i] = (uint32_t)sp[g0] | (uint32_t)sp[g1] << 16;
-            L.b[i] = (uint32_t)bp[g0] | (uint32_t)bp[g1] << 16;
-        }
-    }
+    const int64_t want = row * gpr + u * U::kGroups, last = all * gpr - 2 * U::kWords;  // a tensor has 32 rows at least
+    const int64_t at = want < last ? want : last;
+    L.over = (int)(want - at);
+    load_halves(W.scales + at, L.s);
+    load_halves(W.biases + at, L.b);
     const uint32_t* pw = W.packed + row * kb * BITS;
 #pragma unroll
-    for (int c = 0; c < kUnit; ++c) load_block<BITS>(pw + min(4 * (u * kUnit + c) + g, kb - 1) * BITS, L.w[c]);
+    for (int c = 0; c < kUnit<BITS>; ++c)
+        load_block<BITS>(pw + min(4 * (u * kUnit<BITS> + c) + g, kb - 1) * BITS, L.w[c]);
+}
+
+// The window of a row's last unit, which `there` groups of it fill, moved to its place and masked.
+template <int WORDS> __device__ __forceinline__ void mend_window(uint32_t (&w)[WORDS], int over, int there) {
+#pragma unroll
+    for (int by = 1; by < WORDS; by *= 2)
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = over & 2 * by ? (i + by < WORDS ? w[i + by] : 0u) : w[i];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        w[i] = over & 1 ? __builtin_amdgcn_alignbit(i + 1 < WORDS ? w[i + 1] : 0u, w[i], 16) : w[i];
+        w[i] &= there >= 2 * i + 2 ? ~0u : there == 2 * i + 1 ? 0xffffu : 0u;
+    }
 }
 
 // ---- products ---------------------------------------------------------------------------------------
 
-// acc[m] += x . (unit of weight m)^T for both weights. xa: the lane's row of x in LDS at the unit's first
-// code, xs: the sums of x of the unit's groups ([group][16 rows], at the lane's four result rows).
-template <int BITS, int GSHIFT, bool F16>
-__device__ __forceinline__ void unit_product(const UnitLoads<BITS, GSHIFT> (&L)[2], const uint8_t* xa, const float* xs,
-                                             f32x4 (&acc)[2]) {
+// acc += x . (unit of a weight)^T. xa: the lane's row of x in LDS at the unit's first code, xs: the sums of x of the
+// unit's groups ([group][16 rows], at the lane's four result rows), there: groups of the row from the unit on.
+// SUMS: sums of x a group (16 rows', or 1 where all rows are the same).
+template <int BITS, int GSHIFT, bool F16, int SUMS = kTileRows>
+__device__ __forceinline__ void unit_product(UnitLoads<BITS, GSHIFT>& L, const uint8_t* xa, const float* xs, int there,
+                                             const CodeConsts& cc, f32x4& acc) {
     constexpr int kEach = 1 << GSHIFT;  // products a group
+    if (there < 2 * UnitLoads<BITS, GSHIFT>::kWords) {
+        mend_window(L.s, L.over, there);
+        mend_window(L.b, L.over, there);
+    }
 #pragma unroll
-    for (int c = 0; c < kUnit; ++c) {
-        op8<F16> o[2][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) chunk_operands<F16, BITS, GSHIFT>(L[m].w[c], o[m]);
+    for (int c = 0; c < kUnit<BITS>; ++c) {
+        op8<F16> o[4];
+        chunk_operands<F16, BITS, GSHIFT>(L.w[c], cc, o);
 #pragma unroll
         for (int p = 0; p < (4 >> GSHIFT); ++p) {
-            f32x4 d[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+            f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int step = p * kEach + i;
-                const op8<F16> a = *reinterpret_cast<const op8<F16>*>(xa + 256 * c + 2 * x_step_offset<GSHIFT>(step));
-#pragma unroll
-                for (int m = 0; m < 2; ++m) d[m] = mfma16x16x32<F16>(a, o[m][step], d[m]);
+                d = mfma16x16x32<F16>(*reinterpret_cast<const op8<F16>*>(xa + 256 * c + 2 * x_step_offset<GSHIFT>(step)),
+                                      o[step], d);
             }
             const int grp = (4 * c >> GSHIFT) + p;
-            const f32x4 sum = *reinterpret_cast<const f32x4*>(xs + grp * kTileRows);
+            f32x4 sum;
+            if constexpr (SUMS == 1) sum = f32x4{xs[grp], xs[grp], xs[grp], xs[grp]};
+            else sum = *reinterpret_cast<const f32x4*>(xs + grp * SUMS);
+            const float s = half_to_f32<F16>(L.s[grp >> 1] >> (16 * (grp & 1)));
+            const float b = half_to_f32<F16>(L.b[grp >> 1] >> (16 * (grp & 1)));
+            const float beta = __builtin_fmaf(-kCodeBase<F16, BITS>, s, b);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float s = half_to_f32<F16>(L[m].s[grp >> 1] >> (16 * (grp & 1)));
-                const float b = half_to_f32<F16>(L[m].b[grp >> 1] >> (16 * (grp & 1)));
-                const float beta = __builtin_fmaf(-kCodeBase<F16, BITS>, s, b);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[m][v] = __builtin_fmaf(s, d[m][v], __builtin_fmaf(beta, sum[v], acc[m][v]));
-            }
+            for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(s, d[v], __builtin_fmaf(beta, sum[v], acc[v]));
         }
     }
 }
 
-// Pairs of the expert e whose rank lies in [first, first + count) into rows[0 ..), by one wave; returns
-// the expert's pairs up to that point or more.
-__device__ __forceinline__ int list_rows(const int32_t* chosen, int64_t pairs, int e, int first, int count, int lane,
-                                         int* rows) {
+// Walks items (turn, i), 0 <= i < each, in order, with the next two in the registers A and B (which hold the first two
+// at the start). The loads in the loop have no conditions: the compiler counts those on their way to wait for the ones
+// it needs, and with a branch around some would wait for all. So the last one may repeat an item that is there.
+template <typename Unit, typename Load, typename Take>
+__device__ __forceinline__ void pipeline(int items, int each, Unit (&A)[2], Unit (&B)[2], Load load, Take take) {
+    int t0 = 0, i0 = 0, t1 = 0, i1 = 0;  // the items in A and B
+    auto advance = [&](int& t, int& i) {
+        if (++i >= each) {
+            i = 0;
+            ++t;
+        }
+    };
+    advance(t1, i1);
+    int n = 0;
+    for (; n + 2 < items; n += 2) {
+        int t = t1, i = i1;
+        advance(t, i);
+        take(A, t0, i0);
+        load(A, t, i);
+        t0 = t;
+        i0 = i;
+        if (n + 3 < items) advance(t, i);
+        take(B, t1, i1);
+        load(B, t, i);
+        t1 = t;
+        i1 = i;
+    }
+    take(A, t0, i0);
+    if (n + 1 < items) take(B, t1, i1);
+}
+
+// Pairs of expert e whose rank lies in [first, first + count) into rows[0 ..), by the whole workgroup; returns how
+// many the expert has, up to that point or more. Eight pairs a thread at a time, all of them loaded together;
+// counts: LDS for the hits of each 64 of them.
+__device__ __forceinline__ int list_rows(const int32_t* chosen, int64_t pairs, int e, int first, int count, int tid,
+                                         int* counts, int* rows) {
+    const int lane = tid & 63, wave = tid >> 6;
     int rank = 0;
-    for (int64_t base = 0; base < pairs && rank <= first + count; base += 256) {
-        bool mine[4];
+    for (int64_t base = 0; base < pairs && rank <= first + count; base += 8 * kFewThreads) {
+        bool mine[8];
+        uint64_t hits[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t p = base + 64 * i + lane;
+        for (int i = 0; i < 8; ++i) {
+            const int64_t p = base + i * kFewThreads + tid;
             mine[i] = p < pairs && chosen[p < pairs ? p : 0] == e;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint64_t hits = __builtin_amdgcn_ballot_w64(mine[i]);
-            const int at = rank + __builtin_popcountll(hits & ((1ull << lane) - 1)) - first;
-            if (mine[i] && at >= 0 && at < count) rows[at] = (int)(base + 64 * i + lane);
-            rank += __builtin_popcountll(hits);
+        for (int i = 0; i < 8; ++i) {
+            hits[i] = __builtin_amdgcn_ballot_w64(mine[i]);
+            if (lane == 0) counts[i * kFewWaves + wave] = __builtin_popcountll(hits[i]);
         }
+        __syncthreads();
+        const int own = lane < 8 * kFewWaves ? counts[lane] : 0;
+        const int upto = wave_scan(own);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int before = rank - first + __shfl(upto - own, i * kFewWaves + wave, 64);
+            const int at = before + __builtin_popcountll(hits[i] & ((1ull << lane) - 1));
+            if (mine[i] && at >= 0 && at < count) rows[at] = (int)(base + i * kFewThreads + tid);
+        }
+        rank += __shfl(upto, 63, 64);
+        __syncthreads();  // rows are there; counts are written again
     }
     return rank;
 }
 
 // DOWN = false: gate and up, h out (16-bit). DOWN = true: two neighbouring tiles of the down weight, rows
 // of d out (float32, times the pair's weight).
+//
+// A workgroup has x of up to 16 rows of one expert in LDS. Its waves walk 16-row tiles of the two weights, each
+// wave a tile of its own, or ksplit waves the parts of K of one tile where there are few tiles (their sums meet in
+// LDS). A wave's units of 256 codes, over all its tiles, are one sequence with the next two always on their way,
+// also while the workgroup looks for its rows and loads x.
 template <int BITS, int GSHIFT, bool F16, bool DOWN>
-__global__ __launch_bounds__(64 * kFewWaves) void moe_few_kernel(FewArgs a) {
+__global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ int rows[kTileRows];
-    __shared__ int found;
+    __shared__ int counts[8 * kFewWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     constexpr int kOct = 4 << GSHIFT;  // octets of x a group
-    int e = blockIdx.y;
-    if (a.by_pair) {
-        e = a.chosen[blockIdx.y];
-        if ((uint32_t)e >= (uint32_t)a.experts) return;
-        bool before = false;  // the first pair of an expert works for all of them
-        for (int base = 0; base < (int)blockIdx.y; base += 64)
-            before |= base + lane < (int)blockIdx.y && a.chosen[min(base + lane, (int)blockIdx.y)] == e;
-        if (__builtin_amdgcn_ballot_w64(before)) return;
-    }
+    const int e = blockIdx.y;
     const int pitch = 2 * a.kpad + 16;  // 16 rows at one offset fall on distinct banks
     uint8_t* xl = smem;
     float* xs = reinterpret_cast<float*>(smem + (size_t)a.rows * pitch);
     float* red = xs + (a.kpad >> (5 + GSHIFT)) * kTileRows;
     const int kb = a.k / 32, octets = a.kpad / 8;
-    const int tile_n = DOWN ? 32 : 16;
-    const int tiles = (a.n + tile_n - 1) / tile_n;
+    constexpr int kTileN = DOWN ? 32 : 16;
+    const int tiles = (a.n + kTileN - 1) / kTileN;
     const int side = kFewWaves / a.ksplit;  // tiles at a time
     const int ks = wave % a.ksplit;
-    const int units = a.kpad / (128 * kUnit), each = (units + a.ksplit - 1) / a.ksplit;
+    const int units = a.kpad / (128 * kUnit<BITS>), each = (units + a.ksplit - 1) / a.ksplit;
+    const int u0 = ks * each;                                // this wave's units of a tile: u0 .. u0 + each - 1
+    const int t0 = blockIdx.x * side + wave / a.ksplit;      // and tiles: t0, t0 + step, ...
+    const int step = gridDim.x * side;
+    const int turns = (tiles - (int)blockIdx.x * side + step - 1) / step;  // the same for all waves
+
+    typedef UnitLoads<BITS, GSHIFT> Unit;
+    // Item (turn, i): unit u0 + i of tile t0 + turn step. Items past the row's end or the last tile repeat others.
+    auto load = [&](Unit (&L)[2], int turn, int i) {
+        const int n0 = min(t0 + turn * step, tiles - 1) * kTileN + r16;
+        const int64_t row0 = (int64_t)e * a.n + min(n0, a.n - 1);
+        const int64_t row1 = DOWN ? (int64_t)e * a.n + min(n0 + 16, a.n - 1) : row0;
+        const int u = min(u0 + i, units - 1);
+        load_unit(L[0], a.w0, row0, (int64_t)a.experts * a.n, u, kb, g);
+        load_unit(L[1], DOWN ? a.w0 : a.w1, row1, (int64_t)a.experts * a.n, u, kb, g);
+    };
+    Unit A[2], B[2];
+    const CodeConsts cc = make_code_consts<F16>();
 
     for (int first = 0;; first += a.rows) {
-        if (wave == 0) {
-            const int n = list_rows(a.chosen, a.pairs, e, first, a.rows, lane, rows);
-            if (lane == 0) found = n;
-        }
-        __syncthreads();
-        const int total = found;
+        load(A, 0, 0);
+        if (turns * each > 1) load(B, each > 1 ? 0 : 1, each > 1 ? 1 : 0);
+        const int total = list_rows(a.chosen, a.pairs, e, first, a.rows, tid, counts, rows);
         if (first >= total) return;
         const int nr = min(a.rows, total - first);
         // x of the tile's rows, and its groups' sums
-        for (int i = tid; i < nr * octets; i += 64 * kFewWaves) {
+        for (int i = tid; i < nr * octets; i += kFewThreads) {
             const int r = i / octets, o = i % octets;
             const int64_t src = DOWN ? rows[r] : rows[r] / a.top_k;
             u32x4a v = u32x4a{0u, 0u, 0u, 0u};
@@ -301,31 +379,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_few_kernel(FewArgs a) {
         }
         __syncthreads();
         const uint8_t* xa = xl + (size_t)min(r16, a.rows - 1) * pitch + 2 * x_lane_offset<GSHIFT>(g);
-        for (int t0 = blockIdx.x * side; t0 < tiles; t0 += gridDim.x * side) {
-            const int tile = t0 + wave / a.ksplit;
-            f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-            const int n0 = tile * tile_n + r16;
-            const int64_t row0 = (int64_t)e * a.n + min(n0, a.n - 1);
-            const int64_t row1 = DOWN ? (int64_t)e * a.n + min(n0 + 16, a.n - 1) : row0;
-            for (int u = ks * each; u < min(units, (ks + 1) * each); ++u) {
-                UnitLoads<BITS, GSHIFT> L[2];
-                load_unit(L[0], a.w0, row0, u, kb, g);
-                load_unit(L[1], DOWN ? a.w0 : a.w1, row1, u, kb, g);
-                unit_product<BITS, GSHIFT, F16>(L, xa + (size_t)u * (256 * kUnit),
-                                                xs + u * UnitLoads<BITS, GSHIFT>::kGroups * kTileRows + 4 * g, acc);
-            }
-            if (a.ksplit > 1) {  // sums over the waves of the tile, in order
-                __syncthreads();
+        f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        auto finish = [&](int turn) {  // the tile's sums are complete
+            if (a.ksplit > 1) {        // over its waves, in order
 #pragma unroll
                 for (int m = 0; m < 2; ++m) *reinterpret_cast<f32x4*>(red + ((wave * 2 + m) * 64 + lane) * 4) = acc[m];
                 __syncthreads();
                 if (ks == 0)
+#pragma unroll 1
                     for (int w = 1; w < a.ksplit; ++w)
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
                             acc[m] += *reinterpret_cast<const f32x4*>(red + (((wave + w) * 2 + m) * 64 + lane) * 4);
+                __syncthreads();  // red is written again
             }
             if (ks == 0) {
+                const int n0 = (t0 + turn * step) * kTileN + r16;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int r = 4 * g + v;
@@ -342,8 +411,163 @@ __global__ __launch_bounds__(64 * kFewWaves) void moe_few_kernel(FewArgs a) {
                     }
                 }
             }
+            acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        };
+        auto take = [&](Unit (&L)[2], int turn, int i) {
+            const int u = u0 + i;
+            if (u < units) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    unit_product<BITS, GSHIFT, F16>(L[m], xa + (size_t)u * (256 * kUnit<BITS>),
+                                                    xs + u * Unit::kGroups * kTileRows + 4 * g,
+                                                    (kb >> GSHIFT) - u * Unit::kGroups, cc, acc[m]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if (i == each - 1) finish(turn);
+        };
+        const int items = turns * each;
+        pipeline(items, each, A, B, load, take);
+        __syncthreads();  // rows and x are written again
+    }
+}
+
+// ---- few pairs --------------------------------------------------------------------------------------
+//
+// Where the pairs are few beside the experts, hardly any two name the same one: each pair works alone, without a
+// search for the rows of its expert, and the waves of a workgroup take the pairs of a token in the second product, so
+// that their sum needs no launch of its own. What counts is how many loads depend on each other: the pair's expert, then
+// its weights and x together.
+
+// One row of k values as operands: in LDS at xl (all 16 operand rows read it), its groups' sums at xs.
+template <int BITS, int GSHIFT, bool F16>
+__device__ __forceinline__ void stage_row(const uint16_t* x, int k, int kpad, uint8_t* xl, float* xs, int from, int by) {
+    constexpr int kOct = 4 << GSHIFT;
+    for (int o = from; o < kpad / 8; o += by) {
+        u32x4a v = u32x4a{0u, 0u, 0u, 0u};
+        if (8 * o < k) {
+            const u32x4h h = *reinterpret_cast<const u32x4h*>(x + 8 * o);
+            v = u32x4a{h.x, h.y, h.z, h.w};
         }
-        __syncthreads();  // rows, x and red are written again
+        float sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += half_to_f32<F16>(v[q]) + half_to_f32<F16>(v[q] >> 16);
+#pragma unroll
+        for (int d = 1; d < kOct; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        if (o % kOct == 0) xs[o / kOct] = sum;
+        if constexpr (BITS == 4)
+            v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                       __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+        *reinterpret_cast<u32x4a*>(xl + 16 * o) = v;
+    }
+}
+
+// h of pair blockIdx.y, 16 columns a workgroup, whose waves share K.
+template <int BITS, int GSHIFT, bool F16>
+__global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_pair_kernel(FewArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    __shared__ f32x2 red[kFewWaves][16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int64_t p = blockIdx.y;
+    const int e = a.chosen[p];
+    if ((uint32_t)e >= (uint32_t)a.experts) return;
+    uint8_t* xl = smem;
+    float* xs = reinterpret_cast<float*>(smem + 2 * a.kpad);
+    const int kb = a.k / 32, units = a.kpad / (128 * kUnit<BITS>), each = (units + kFewWaves - 1) / kFewWaves;
+    const int u0 = wave * each;
+    typedef UnitLoads<BITS, GSHIFT> Unit;
+    const int n0 = blockIdx.x * 16 + r16;
+    const int64_t row = (int64_t)e * a.n + min(n0, a.n - 1), all = (int64_t)a.experts * a.n;
+    auto load = [&](Unit (&L)[2], int, int i) {
+        const int u = min(u0 + i, units - 1);
+        load_unit(L[0], a.w0, row, all, u, kb, g);
+        load_unit(L[1], a.w1, row, all, u, kb, g);
+    };
+    Unit A[2], B[2];
+    const CodeConsts cc = make_code_consts<F16>();
+    load(A, 0, 0);
+    if (each > 1) load(B, 0, 1);
+    stage_row<BITS, GSHIFT, F16>(a.x + p / a.top_k * a.k, a.k, a.kpad, xl, xs, tid, kFewThreads);
+    __syncthreads();
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    const uint8_t* xa = xl + 2 * x_lane_offset<GSHIFT>(g);
+    pipeline(each, each, A, B, load, [&](Unit (&L)[2], int, int i) {
+        const int u = u0 + i;
+        if (u >= units) return;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            unit_product<BITS, GSHIFT, F16, 1>(L[m], xa + (size_t)u * (256 * kUnit<BITS>), xs + u * Unit::kGroups,
+                                               (kb >> GSHIFT) - u * Unit::kGroups, cc, acc[m]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    });
+    if (g == 0) red[wave][r16] = f32x2{acc[0][0], acc[1][0]};  // all result rows are the same
+    __syncthreads();
+    if (tid < 16 && n0 < a.n) {
+        f32x2 sum = red[0][tid];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) sum += red[w][tid];
+        static_cast<uint16_t*>(a.out)[p * a.n + n0] = f32_to_half_bits<F16>(silu_f32(sum.x) * sum.y);
+    }
+}
+
+constexpr int kPairWaves = 8;
+
+// y of token blockIdx.y, 32 columns a workgroup: the waves take the token's pairs in turn, each with all of K.
+template <int BITS, int GSHIFT, bool F16>
+__global__ __launch_bounds__(64 * kPairWaves) void moe_pair_down_kernel(FewArgs a, const uint16_t* resid) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int64_t t = blockIdx.y;
+    const int kb = a.k / 32, units = a.kpad / (128 * kUnit<BITS>);
+    const int region = 2 * a.kpad + (a.kpad >> (5 + GSHIFT)) * 4;
+    uint8_t* xl = smem + wave * region;
+    float* xs = reinterpret_cast<float*>(xl + 2 * a.kpad);
+    float* red = reinterpret_cast<float*>(smem + kPairWaves * region);  // [top_k][32]
+    typedef UnitLoads<BITS, GSHIFT> Unit;
+    const int n0 = blockIdx.x * 32 + r16;
+    const CodeConsts cc = make_code_consts<F16>();
+    for (int j = wave; j < a.top_k; j += kPairWaves) {
+        const int64_t p = t * a.top_k + j;
+        const int e = __builtin_amdgcn_readfirstlane(a.chosen[p]);
+        f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        float w = 0.f;
+        if ((uint32_t)e < (uint32_t)a.experts) {
+            const int64_t row0 = (int64_t)e * a.n + min(n0, a.n - 1), row1 = (int64_t)e * a.n + min(n0 + 16, a.n - 1);
+            const int64_t all = (int64_t)a.experts * a.n;
+            auto load = [&](Unit (&L)[2], int, int i) {
+                load_unit(L[0], a.w0, row0, all, i, kb, g);
+                load_unit(L[1], a.w0, row1, all, i, kb, g);
+            };
+            Unit A[2], B[2];
+            load(A, 0, 0);
+            if (units > 1) load(B, 0, 1);
+            w = a.weights[p];
+            stage_row<BITS, GSHIFT, F16>(a.x + p * a.k, a.k, a.kpad, xl, xs, lane, 64);  // the wave's own: no barrier
+            const uint8_t* xa = xl + 2 * x_lane_offset<GSHIFT>(g);
+            pipeline(units, units, A, B, load, [&](Unit (&L)[2], int, int u) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    unit_product<BITS, GSHIFT, F16, 1>(L[m], xa + (size_t)u * (256 * kUnit<BITS>), xs + u * Unit::kGroups,
+                                                       (kb >> GSHIFT) - u * Unit::kGroups, cc, acc[m]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            });
+        }
+        if (g < 2) red[j * 32 + 16 * g + r16] = w * acc[g][0];
+    }
+    __syncthreads();
+    const int col = blockIdx.x * 32 + tid;
+    if (tid < 32 && col < a.n) {
+        const int64_t at = t * a.n + col;
+        float sum = resid ? half_to_f32<F16>(resid[at]) : 0.f;
+        for (int j = 0; j < a.top_k; ++j)
+            if ((uint32_t)a.chosen[t * a.top_k + j] < (uint32_t)a.experts) sum += red[j * 32 + tid];
+        static_cast<uint16_t*>(a.out)[at] = f32_to_half_bits<F16>(sum);
     }
 }
 
@@ -390,21 +614,28 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* d, const 
 inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 template <int BITS, int GSHIFT, bool F16, bool DOWN>
-hipError_t launch_few_kernel(FewArgs a, int64_t tokens, hipStream_t stream) {
-    a.kpad = (int)round_up(a.k, 128 * kUnit);
+hipError_t launch_few_kernel(FewArgs a, hipStream_t stream) {
+    a.kpad = (int)round_up(a.k, 128 * kUnit<BITS>);
     const int pitch = 2 * a.kpad + 16;
     const int sums = (a.kpad >> (5 + GSHIFT)) * kTileRows * 4;
     constexpr int kRed = kFewWaves * 2 * 64 * 16;
-    a.rows = (int)(a.pairs < kTileRows ? a.pairs : kTileRows);
+    // Rows of x a pass: twice the average of the experts that are used, as a smaller x lets more workgroups share a
+    // compute unit (16 rows of 2048 values: two, 8 rows: three).
+    const int64_t used = std::min(a.pairs, (int64_t)a.experts);
+    a.rows = (int)std::min((int64_t)kTileRows, std::max(std::min(a.pairs, (int64_t)4), 2 * a.pairs / used));
     while (a.rows > 1 && a.rows * pitch + sums + kRed > 150 * 1024) a.rows = (a.rows + 1) / 2;
     const int lds = a.rows * pitch + sums + kRed;
     const int tiles = (a.n + (DOWN ? 31 : 15)) / (DOWN ? 32 : 16);
-    a.by_pair = a.pairs < a.experts;
-    const int slots = (int)(a.by_pair ? a.pairs : a.experts);
-    a.ksplit = kFewWaves;
+    const int64_t slots = used;  // experts that have work, at most
+    // Waves that share a tile: as many as it takes to give all of them work. Workgroups of
+    // an expert: as many as run at once, each over several tiles, so that x is loaded few times.
+    const int64_t room = (int64_t)device_cu_count() * std::min((int64_t)kFewBlocks, (int64_t)(160 * 1024 / (lds + 512)));
+    a.ksplit = 1;
+    while (a.ksplit < kFewWaves && slots * tiles * a.ksplit < room * kFewWaves) a.ksplit *= 2;
     const int side = kFewWaves / a.ksplit;
-    const int gx = (tiles + side - 1) / side;
-    moe_few_kernel<BITS, GSHIFT, F16, DOWN><<<dim3(gx, slots), dim3(64 * kFewWaves), lds, stream>>>(a);
+    const int64_t most = (tiles + side - 1) / side;
+    const int64_t gx = std::max((int64_t)1, std::min(most, (room + slots - 1) / slots));
+    moe_few_kernel<BITS, GSHIFT, F16, DOWN><<<dim3((unsigned)gx, (unsigned)a.experts), dim3(kFewThreads), lds, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -413,6 +644,30 @@ hipError_t launch_combine(const MoeArgs& a, const float* d, hipStream_t stream) 
     const int64_t threads = a.tokens * (a.width / 8);
     moe_combine_kernel<F16><<<dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream>>>(
         d, a.chosen, a.resid, a.y, a.tokens, a.width, d ? a.top_k : 0, a.experts);
+    return hipGetLastError();
+}
+
+// Whether each pair works alone: the pairs are few beside the experts, and their rows fit LDS.
+inline bool pair_path(const MoeArgs& a) {
+    return a.tokens * a.top_k * 4 <= a.experts && a.hidden <= 4096 && a.top_k <= 64;
+}
+
+template <int BITS, int GSHIFT, bool F16>
+hipError_t launch_pairs(const MoeArgs& a, FewArgs f, hipStream_t stream) {
+    f.kpad = (int)round_up(f.k, 128 * kUnit<BITS>);
+    moe_pair_kernel<BITS, GSHIFT, F16><<<dim3((unsigned)((f.n + 15) / 16), (unsigned)f.pairs), dim3(kFewThreads),
+                                         2 * f.kpad + (f.kpad >> (5 + GSHIFT)) * 4, stream>>>(f);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    f.x = static_cast<const uint16_t*>(f.out);
+    f.w0 = a.down;
+    f.out = a.y;
+    f.k = a.hidden;
+    f.n = a.width;
+    f.kpad = (int)round_up(f.k, 128 * kUnit<BITS>);
+    const int lds = kPairWaves * (2 * f.kpad + (f.kpad >> (5 + GSHIFT)) * 4) + a.top_k * 32 * 4;
+    moe_pair_down_kernel<BITS, GSHIFT, F16><<<dim3((unsigned)((f.n + 31) / 32), (unsigned)a.tokens), dim3(64 * kPairWaves),
+                                              lds, stream>>>(f, a.resid);
     return hipGetLastError();
 }
 
@@ -433,14 +688,15 @@ hipError_t launch_few(const MoeArgs& a, hipStream_t stream) {
     f.out = h;
     f.k = a.width;
     f.n = a.hidden;
-    hipError_t e = launch_few_kernel<BITS, GSHIFT, F16, false>(f, a.tokens, stream);
+    if (pair_path(a)) return launch_pairs<BITS, GSHIFT, F16>(a, f, stream);
+    hipError_t e = launch_few_kernel<BITS, GSHIFT, F16, false>(f, stream);
     if (e != hipSuccess) return e;
     f.x = h;
     f.w0 = f.w1 = a.down;
     f.out = d;
     f.k = a.hidden;
     f.n = a.width;
-    e = launch_few_kernel<BITS, GSHIFT, F16, true>(f, a.tokens, stream);
+    e = launch_few_kernel<BITS, GSHIFT, F16, true>(f, stream);
     if (e != hipSuccess) return e;
     return launch_combine<F16>(a, d, stream);
 }

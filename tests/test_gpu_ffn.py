@@ -109,7 +109,8 @@ def check_moe(i, resid=None, what=""):
 @pytest.mark.parametrize("bits", [1, 2, 3, 4, 5, 6, 8])
 def test_moe_formats(dtype, group, bits):
     gen = gen_of("moe", group, bits)
-    for tokens, experts, top_k, hidden, width in [(1, 4, 2, 128, 256), (21, 3, 2, 384, 640), (90, 3, 2, 384, 640)]:
+    for tokens, experts, top_k, hidden, width in [(1, 4, 2, 128, 256), (1, 12, 3, 384, 640), (21, 3, 2, 384, 640),
+                                                  (90, 3, 2, 384, 640)]:
         what = f"moe {bits} bits g{group} {dtype} {tokens} tokens {experts} experts [{hidden}, {width}]"
         banner(what)
         i = moe_inputs(gen, tokens, experts, top_k, hidden, width, bits, group, dtype)
@@ -123,7 +124,9 @@ def test_moe_formats(dtype, group, bits):
                           (300, 4, 2, 192, 320, 4, 64), (1000, 5, 3, 64, 128, 4, 64), (7, 60, 4, 352, 416, 5, 32),
                           (3, 2, 2, 128, 8192, 4, 64), (18, 2, 2, 9216, 128, 4, 128), (130, 300, 4, 64, 64, 2, 64), (700, 3, 1, 96, 160, 4, 32),
                           (193, 1, 1, 64, 128, 3, 64), (200, 4, 4, 32, 32, 4, 32), (250, 8, 2, 256, 2176, 6, 128),
-                          (130, 5, 2, 1056, 288, 8, 32)])
+                          (130, 5, 2, 1056, 288, 8, 32), (1, 128, 8, 768, 2048, 4, 64), (2, 64, 8, 96, 160, 5, 32),
+                          (3, 48, 4, 1056, 288, 8, 32), (1, 300, 60, 64, 128, 3, 64), (1, 4, 1, 4096, 32, 4, 32),
+                          (1, 9, 2, 4224, 128, 4, 128), (5, 160, 8, 32, 4160, 2, 32)])
 def test_moe_sizes(dtype, tokens, experts, top_k, hidden, width, bits, group):
     gen = gen_of("sizes", tokens, experts, hidden)
     what = f"moe {tokens} tokens {top_k} of {experts} [{hidden}, {width}] {bits} bits g{group} {dtype}"
