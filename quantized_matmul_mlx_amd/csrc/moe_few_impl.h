@@ -207,17 +207,31 @@ template <int WORDS> __device__ __forceinline__ void mend_window(uint32_t (&w)[W
 // unit's groups ([group][16 rows], at the lane's four result rows), there: groups of the row from the unit on.
 // SUMS: sums of x a group (16 rows', or 1 where all rows are the same).
 template <int BITS, int GSHIFT, bool F16, int SUMS = kTileRows>
-__device__ __forceinline__ void unit_product(UnitLoads<BITS, GSHIFT>& L, const uint8_t* xa, const float* xs, int there,
+__device__ __forceinline__ void unit_product(const UnitLoads<BITS, GSHIFT>& L, const uint8_t* xa, const float* xs, int there,
                                              const CodeConsts& cc, f32x4& acc) {
     constexpr int kEach = 1 << GSHIFT;  // products a group
-    if (there < 2 * UnitLoads<BITS, GSHIFT>::kWords) {
-        mend_window(L.s, L.over, there);
-        mend_window(L.b, L.over, there);
+    // copies: were the loaded registers written here, the compiler would copy each load and wait for it there
+    constexpr int kWords = UnitLoads<BITS, GSHIFT>::kWords;
+    uint32_t sw[kWords], bw[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        sw[i] = L.s[i];
+        bw[i] = L.b[i];
+    }
+    if (there < 2 * kWords) {
+        mend_window(sw, L.over, there);
+        mend_window(bw, L.over, there);
     }
 #pragma unroll
     for (int c = 0; c < kUnit<BITS>; ++c) {
         op8<F16> o[4];
-        chunk_operands<F16, BITS, GSHIFT>(L.w[c], cc, o);
+        uint32_t w[BITS];
+#pragma unroll
+        for (int i = 0; i < BITS; ++i) {
+            w[i] = L.w[c][i];
+            asm volatile("" : "+v"(w[i]));  // here, not where the loads are issued, which would wait for them
+        }
+        chunk_operands<F16, BITS, GSHIFT>(w, cc, o);
 #pragma unroll
         for (int p = 0; p < (4 >> GSHIFT); ++p) {
             f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -231,8 +245,8 @@ __device__ __forceinline__ void unit_product(UnitLoads<BITS, GSHIFT>& L, const u
             f32x4 sum;
             if constexpr (SUMS == 1) sum = f32x4{xs[grp], xs[grp], xs[grp], xs[grp]};
             else sum = *reinterpret_cast<const f32x4*>(xs + grp * SUMS);
-            const float s = half_to_f32<F16>(L.s[grp >> 1] >> (16 * (grp & 1)));
-            const float b = half_to_f32<F16>(L.b[grp >> 1] >> (16 * (grp & 1)));
+            const float s = half_to_f32<F16>(sw[grp >> 1] >> (16 * (grp & 1)));
+            const float b = half_to_f32<F16>(bw[grp >> 1] >> (16 * (grp & 1)));
             const float beta = __builtin_fmaf(-kCodeBase<F16, BITS>, s, b);
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(s, d[v], __builtin_fmaf(beta, sum[v], acc[v]));
@@ -240,11 +254,29 @@ __device__ __forceinline__ void unit_product(UnitLoads<BITS, GSHIFT>& L, const u
     }
 }
 
+// Octet o of a row of x (0 where it is not there) into LDS: the values at xl, in the order of 4-bit operands, and the
+// sum of its group at xs, SUMS apart; the lanes of a group come together.
+template <int BITS, int GSHIFT, bool F16, int SUMS>
+__device__ __forceinline__ void stage_octet(u32x4h h, bool there, int o, uint8_t* xl, float* xs) {
+    constexpr int kOct = 4 << GSHIFT;  // octets of a group
+    u32x4a v = there ? u32x4a{h.x, h.y, h.z, h.w} : u32x4a{0u, 0u, 0u, 0u};
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum += half_to_f32<F16>(v[q]) + half_to_f32<F16>(v[q] >> 16);
+#pragma unroll
+    for (int d = 1; d < kOct; d <<= 1) sum += __shfl_xor(sum, d, 64);
+    if (o % kOct == 0) xs[o / kOct * SUMS] = sum;
+    if constexpr (BITS == 4)
+        v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                   __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+    *reinterpret_cast<u32x4a*>(xl + 16 * o) = v;
+}
+
 // Walks items (turn, i), 0 <= i < each, in order, with the next two in the registers A and B (which hold the first two
 // at the start). The loads in the loop have no conditions: the compiler counts those on their way to wait for the ones
 // it needs, and with a branch around some would wait for all. So the last one may repeat an item that is there.
-template <typename Unit, typename Load, typename Take>
-__device__ __forceinline__ void pipeline(int items, int each, Unit (&A)[2], Unit (&B)[2], Load load, Take take) {
+template <typename Units, typename Load, typename Take>
+__device__ __forceinline__ void pipeline(int items, int each, Units& A, Units& B, Load load, Take take) {
     int t0 = 0, i0 = 0, t1 = 0, i1 = 0;  // the items in A and B
     auto advance = [&](int& t, int& i) {
         if (++i >= each) {
@@ -284,7 +316,8 @@ __device__ __forceinline__ int list_rows(const int32_t* chosen, int64_t pairs, i
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t p = base + i * kFewThreads + tid;
-            mine[i] = p < pairs && chosen[p < pairs ? p : 0] == e;
+            mine[i] = chosen[min(p, pairs - 1)] == e;  // no branch around the load: the eight go out together
+            mine[i] &= p < pairs;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -317,11 +350,11 @@ template <int BITS, int GSHIFT, bool F16, bool DOWN>
 __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ int rows[kTileRows];
+    __shared__ float weight_of[kTileRows];
     __shared__ int counts[8 * kFewWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
-    constexpr int kOct = 4 << GSHIFT;  // octets of x a group
     const int e = blockIdx.y;
     const int pitch = 2 * a.kpad + 16;  // 16 rows at one offset fall on distinct banks
     uint8_t* xl = smem;
@@ -353,29 +386,27 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArg
 
     for (int first = 0;; first += a.rows) {
         load(A, 0, 0);
-        if (turns * each > 1) load(B, each > 1 ? 0 : 1, each > 1 ? 1 : 0);
+        load(B, each > 1 ? 0 : min(1, turns - 1), each > 1 ? 1 : 0);
         const int total = list_rows(a.chosen, a.pairs, e, first, a.rows, tid, counts, rows);
         if (first >= total) return;
         const int nr = min(a.rows, total - first);
+        if constexpr (DOWN)
+            if (tid < nr) weight_of[tid] = a.weights[rows[tid]];
         // x of the tile's rows, and its groups' sums
-        for (int i = tid; i < nr * octets; i += kFewThreads) {
-            const int r = i / octets, o = i % octets;
-            const int64_t src = DOWN ? rows[r] : rows[r] / a.top_k;
-            u32x4a v = u32x4a{0u, 0u, 0u, 0u};
-            if (8 * o < a.k) {
-                const u32x4h h = *reinterpret_cast<const u32x4h*>(a.x + src * a.k + 8 * o);
-                v = u32x4a{h.x, h.y, h.z, h.w};
+        for (int i0 = tid; i0 < nr * octets; i0 += 4 * kFewThreads) {
+            u32x4h h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // four pieces a thread on their way together
+                const int i = min(i0 + q * kFewThreads, nr * octets - 1), r = i / octets, o = min(i % octets, a.k / 8 - 1);
+                const int64_t src = DOWN ? rows[r] : rows[r] / a.top_k;
+                h[q] = *reinterpret_cast<const u32x4h*>(a.x + src * a.k + 8 * o);
             }
-            float sum = 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sum += half_to_f32<F16>(v[q]) + half_to_f32<F16>(v[q] >> 16);
-#pragma unroll
-            for (int d = 1; d < kOct; d <<= 1) sum += __shfl_xor(sum, d, 64);
-            if (o % kOct == 0) xs[o / kOct * kTileRows + r] = sum;
-            if constexpr (BITS == 4)
-                v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                           __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-            *reinterpret_cast<u32x4a*>(xl + (size_t)r * pitch + 16 * o) = v;
+            for (int q = 0; q < 4; ++q) {
+                const int i = i0 + q * kFewThreads, r = i / octets, o = i % octets;
+                if (i < nr * octets)  // whole groups of lanes
+                    stage_octet<BITS, GSHIFT, F16, kTileRows>(h[q], 8 * o < a.k, o, xl + (size_t)r * pitch, xs + r);
+            }
         }
         __syncthreads();
         const uint8_t* xa = xl + (size_t)min(r16, a.rows - 1) * pitch + 2 * x_lane_offset<GSHIFT>(g);
@@ -401,7 +432,7 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArg
                     if (r >= nr) continue;
                     const int64_t p = rows[r];
                     if constexpr (DOWN) {
-                        const float w = a.weights[p];
+                        const float w = weight_of[r];
                         float* d = static_cast<float*>(a.out) + p * a.n;
                         if (n0 < a.n) d[n0] = w * acc[0][v];
                         if (n0 + 16 < a.n) d[n0 + 16] = w * acc[1][v];
@@ -413,7 +444,7 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArg
             }
             acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
         };
-        auto take = [&](Unit (&L)[2], int turn, int i) {
+        auto take = [&](const Unit (&L)[2], int turn, int i) {
             const int u = u0 + i;
             if (u < units) {
 #pragma unroll
@@ -442,23 +473,15 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArg
 // One row of k values as operands: in LDS at xl (all 16 operand rows read it), its groups' sums at xs.
 template <int BITS, int GSHIFT, bool F16>
 __device__ __forceinline__ void stage_row(const uint16_t* x, int k, int kpad, uint8_t* xl, float* xs, int from, int by) {
-    constexpr int kOct = 4 << GSHIFT;
-    for (int o = from; o < kpad / 8; o += by) {
-        u32x4a v = u32x4a{0u, 0u, 0u, 0u};
-        if (8 * o < k) {
-            const u32x4h h = *reinterpret_cast<const u32x4h*>(x + 8 * o);
-            v = u32x4a{h.x, h.y, h.z, h.w};
+    for (int o0 = from; o0 < kpad / 8; o0 += 2 * by) {
+        u32x4h h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) h[q] = *reinterpret_cast<const u32x4h*>(x + 8 * min(o0 + q * by, k / 8 - 1));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int o = o0 + q * by;
+            if (o < kpad / 8) stage_octet<BITS, GSHIFT, F16, 1>(h[q], 8 * o < k, o, xl, xs);
         }
-        float sum = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum += half_to_f32<F16>(v[q]) + half_to_f32<F16>(v[q] >> 16);
-#pragma unroll
-        for (int d = 1; d < kOct; d <<= 1) sum += __shfl_xor(sum, d, 64);
-        if (o % kOct == 0) xs[o / kOct] = sum;
-        if constexpr (BITS == 4)
-            v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                       __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-        *reinterpret_cast<u32x4a*>(xl + 16 * o) = v;
     }
 }
 
@@ -493,7 +516,7 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_pair_kernel(FewAr
     __syncthreads();
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     const uint8_t* xa = xl + 2 * x_lane_offset<GSHIFT>(g);
-    pipeline(each, each, A, B, load, [&](Unit (&L)[2], int, int i) {
+    pipeline(each, each, A, B, load, [&](const Unit (&L)[2], int, int i) {
         const int u = u0 + i;
         if (u >= units) return;
 #pragma unroll
@@ -513,9 +536,9 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_pair_kernel(FewAr
     }
 }
 
-constexpr int kPairWaves = 8;
+constexpr int kPairWaves = 16;
 
-// y of token blockIdx.y, 32 columns a workgroup: the waves take the token's pairs in turn, each with all of K.
+// y of token blockIdx.y, 16 columns a workgroup: pairs of waves take the token's pairs in turn, each wave half of K.
 template <int BITS, int GSHIFT, bool F16>
 __global__ __launch_bounds__(64 * kPairWaves) void moe_pair_down_kernel(FewArgs a, const uint16_t* resid) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -523,50 +546,52 @@ __global__ __launch_bounds__(64 * kPairWaves) void moe_pair_down_kernel(FewArgs 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int64_t t = blockIdx.y;
-    const int kb = a.k / 32, units = a.kpad / (128 * kUnit<BITS>);
+    const int kb = a.k / 32, units = a.kpad / (128 * kUnit<BITS>), each = (units + 1) / 2;
     const int region = 2 * a.kpad + (a.kpad >> (5 + GSHIFT)) * 4;
-    uint8_t* xl = smem + wave * region;
+    uint8_t* xl = smem + (wave >> 1) * region;  // h of the pair, staged by both of its waves
     float* xs = reinterpret_cast<float*>(xl + 2 * a.kpad);
-    float* red = reinterpret_cast<float*>(smem + kPairWaves * region);  // [top_k][32]
+    float* red = reinterpret_cast<float*>(smem + kPairWaves / 2 * region);  // [top_k][2][16]
     typedef UnitLoads<BITS, GSHIFT> Unit;
-    const int n0 = blockIdx.x * 32 + r16;
+    const int n0 = blockIdx.x * 16 + r16;
     const CodeConsts cc = make_code_consts<F16>();
-    for (int j = wave; j < a.top_k; j += kPairWaves) {
-        const int64_t p = t * a.top_k + j;
+    const int rounds = (a.top_k + kPairWaves / 2 - 1) / (kPairWaves / 2);
+    for (int q = 0; q < rounds; ++q) {
+        const int j = q * (kPairWaves / 2) + (wave >> 1);
+        const int64_t p = t * a.top_k + min(j, a.top_k - 1);
         const int e = __builtin_amdgcn_readfirstlane(a.chosen[p]);
-        f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-        float w = 0.f;
-        if ((uint32_t)e < (uint32_t)a.experts) {
-            const int64_t row0 = (int64_t)e * a.n + min(n0, a.n - 1), row1 = (int64_t)e * a.n + min(n0 + 16, a.n - 1);
-            const int64_t all = (int64_t)a.experts * a.n;
-            auto load = [&](Unit (&L)[2], int, int i) {
-                load_unit(L[0], a.w0, row0, all, i, kb, g);
-                load_unit(L[1], a.w0, row1, all, i, kb, g);
-            };
-            Unit A[2], B[2];
-            load(A, 0, 0);
-            if (units > 1) load(B, 0, 1);
-            w = a.weights[p];
-            stage_row<BITS, GSHIFT, F16>(a.x + p * a.k, a.k, a.kpad, xl, xs, lane, 64);  // the wave's own: no barrier
+        const bool there = j < a.top_k && (uint32_t)e < (uint32_t)a.experts;
+        const int64_t all = (int64_t)a.experts * a.n;
+        const int64_t row = (int64_t)(there ? e : 0) * a.n + min(n0, a.n - 1);
+        const int u0 = (wave & 1) * each, mine = there ? min(each, units - u0) : 0;
+        auto load = [&](Unit& L, int, int i) { load_unit(L, a.w0, row, all, min(u0 + i, units - 1), kb, g); };
+        Unit A, B;
+        if (mine > 0) load(A, 0, 0);
+        if (mine > 1) load(B, 0, 1);
+        if (there) stage_row<BITS, GSHIFT, F16>(a.x + p * a.k, a.k, a.kpad, xl, xs, (wave & 1) * 64 + lane, 128);
+        __syncthreads();
+        if (mine > 0) {
+            f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
             const uint8_t* xa = xl + 2 * x_lane_offset<GSHIFT>(g);
-            pipeline(units, units, A, B, load, [&](Unit (&L)[2], int, int u) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    unit_product<BITS, GSHIFT, F16, 1>(L[m], xa + (size_t)u * (256 * kUnit<BITS>), xs + u * Unit::kGroups,
-                                                       (kb >> GSHIFT) - u * Unit::kGroups, cc, acc[m]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            pipeline(mine, mine, A, B, load, [&](const Unit& L, int, int i) {
+                const int u = u0 + i;
+                unit_product<BITS, GSHIFT, F16, 1>(L, xa + (size_t)u * (256 * kUnit<BITS>), xs + u * Unit::kGroups,
+                                                   (kb >> GSHIFT) - u * Unit::kGroups, cc, acc);
             });
+            if (g == 0) red[(j * 2 + (wave & 1)) * 16 + r16] = acc[0];  // all result rows are the same
+        } else if (there && g == 0) {
+            red[(j * 2 + (wave & 1)) * 16 + r16] = 0.f;
         }
-        if (g < 2) red[j * 32 + 16 * g + r16] = w * acc[g][0];
+        __syncthreads();  // red is there; h is staged again
     }
-    __syncthreads();
-    const int col = blockIdx.x * 32 + tid;
-    if (tid < 32 && col < a.n) {
+    const int col = blockIdx.x * 16 + tid;
+    if (tid < 16 && col < a.n) {
         const int64_t at = t * a.n + col;
         float sum = resid ? half_to_f32<F16>(resid[at]) : 0.f;
-        for (int j = 0; j < a.top_k; ++j)
-            if ((uint32_t)a.chosen[t * a.top_k + j] < (uint32_t)a.experts) sum += red[j * 32 + tid];
+        for (int j = 0; j < a.top_k; ++j) {
+            const int64_t p = t * a.top_k + j;
+            if ((uint32_t)a.chosen[p] < (uint32_t)a.experts)
+                sum = __builtin_fmaf(a.weights[p], red[j * 32 + tid] + red[j * 32 + 16 + tid], sum);
+        }
         static_cast<uint16_t*>(a.out)[at] = f32_to_half_bits<F16>(sum);
     }
 }
@@ -619,10 +644,10 @@ hipError_t launch_few_kernel(FewArgs a, hipStream_t stream) {
     const int pitch = 2 * a.kpad + 16;
     const int sums = (a.kpad >> (5 + GSHIFT)) * kTileRows * 4;
     constexpr int kRed = kFewWaves * 2 * 64 * 16;
-    // Rows of x a pass: twice the average of the experts that are used, as a smaller x lets more workgroups share a
-    // compute unit (16 rows of 2048 values: two, 8 rows: three).
+    // Rows of x a pass: 16, or 8 up to an average of 4 rows an expert that is used (a smaller x lets more workgroups
+    // share a compute unit: 16 rows of 2048 values two, 8 rows three).
     const int64_t used = std::min(a.pairs, (int64_t)a.experts);
-    a.rows = (int)std::min((int64_t)kTileRows, std::max(std::min(a.pairs, (int64_t)4), 2 * a.pairs / used));
+    a.rows = (int)std::min(a.pairs, a.pairs <= 4 * used ? (int64_t)8 : (int64_t)kTileRows);
     while (a.rows > 1 && a.rows * pitch + sums + kRed > 150 * 1024) a.rows = (a.rows + 1) / 2;
     const int lds = a.rows * pitch + sums + kRed;
     const int tiles = (a.n + (DOWN ? 31 : 15)) / (DOWN ? 32 : 16);
@@ -634,7 +659,7 @@ hipError_t launch_few_kernel(FewArgs a, hipStream_t stream) {
     while (a.ksplit < kFewWaves && slots * tiles * a.ksplit < room * kFewWaves) a.ksplit *= 2;
     const int side = kFewWaves / a.ksplit;
     const int64_t most = (tiles + side - 1) / side;
-    const int64_t gx = std::max((int64_t)1, std::min(most, (room + slots - 1) / slots));
+    const int64_t gx = std::max((int64_t)1, std::min(most, room / slots));
     moe_few_kernel<BITS, GSHIFT, F16, DOWN><<<dim3((unsigned)gx, (unsigned)a.experts), dim3(kFewThreads), lds, stream>>>(a);
     return hipGetLastError();
 }
@@ -665,8 +690,8 @@ hipError_t launch_pairs(const MoeArgs& a, FewArgs f, hipStream_t stream) {
     f.k = a.hidden;
     f.n = a.width;
     f.kpad = (int)round_up(f.k, 128 * kUnit<BITS>);
-    const int lds = kPairWaves * (2 * f.kpad + (f.kpad >> (5 + GSHIFT)) * 4) + a.top_k * 32 * 4;
-    moe_pair_down_kernel<BITS, GSHIFT, F16><<<dim3((unsigned)((f.n + 31) / 32), (unsigned)a.tokens), dim3(64 * kPairWaves),
+    const int lds = kPairWaves / 2 * (2 * f.kpad + (f.kpad >> (5 + GSHIFT)) * 4) + a.top_k * 32 * 4;
+    moe_pair_down_kernel<BITS, GSHIFT, F16><<<dim3((unsigned)((f.n + 15) / 16), (unsigned)a.tokens), dim3(64 * kPairWaves),
                                               lds, stream>>>(f, a.resid);
     return hipGetLastError();
 }
