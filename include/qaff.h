@@ -569,7 +569,7 @@ qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, i
  *   which the call overwrites (float32 partial sums where few rows split K, joined in a fixed order); may be
  *   null where that size is 0. Results are deterministic.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown y_dtype, null or misaligned pointers (scales 4
- * bytes, y its element size), a short workspace; UNSUPPORTED for m or k of 2^31 or more, n of 2^28 or more.
+ * bytes, y its element size), a short workspace; UNSUPPORTED for m of 2^31 or more, n of 2^28 or more, k above 2^18.
  */
 qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, const uint8_t* w,
                            const float* w_scales, int64_t n, int64_t k, void* workspace,

@@ -20,6 +20,8 @@ uintptr_t esize(qaff_dtype d) { return d == QAFF_F32 ? 4 : 2; }
 
 constexpr int64_t kMaxColumns = 32768;  // of an expert's weights: a row of x and its groups' sums fit a workgroup
 
+constexpr int64_t kMaxBlockK = 1 << 18;  // a workgroup holds the scales of 16 rows of x
+
 qaff_status check_moe_sizes(const char* op, int64_t tokens, int64_t width, int64_t hidden, int64_t top_k,
                             int64_t experts, int32_t group_size, int32_t bits) {
     if (bits < 1 || bits > 8 || bits == 7)
@@ -177,7 +179,7 @@ qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, i
 }
 
 size_t qaff_block_qmm_workspace_size(int64_t m, int64_t n, int64_t k) {
-    if (m <= 0 || n <= 0 || k <= 0 || m >= k2G || n >= 1LL << 28 || k >= k2G) return 0;
+    if (m <= 0 || n <= 0 || k <= 0 || m >= k2G || n >= 1LL << 28 || k > kMaxBlockK) return 0;
     return qaff::block_qmm_workspace(m, n, k);
 }
 
@@ -188,8 +190,9 @@ qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, c
     qaff::set_error("");
     if (!any_dtype(y_dtype)) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", op, (int)y_dtype);
     if (m < 0 || n < 0 || k < 0) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: negative size", op);
-    if (m >= k2G || n >= 1LL << 28 || k >= k2G)
-        return fail(QAFF_ERR_UNSUPPORTED, "%s: 2^31 rows of x or columns, or 2^28 rows of w, or more", op);
+    if (m >= k2G || n >= 1LL << 28 || k > kMaxBlockK)
+        return fail(QAFF_ERR_UNSUPPORTED, "%s: 2^31 rows of x or 2^28 rows of w or more, or above %lld columns", op,
+                    (long long)kMaxBlockK);
     if (m == 0 || n == 0) return QAFF_OK;
     qaff_status st = check_ptr(op, "y", y, esize(y_dtype));
     if (st == QAFF_OK && k > 0) {

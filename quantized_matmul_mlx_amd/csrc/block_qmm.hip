@@ -8,6 +8,9 @@
 // by 1.4e-5 of the sum for normal values, by 1.6e-4 of the sum of magnitudes at most for random codes).
 #include "ffn.h"
 #include "mfma16.h"
+#include "wave.h"
+
+#include <algorithm>
 
 namespace qaff {
 namespace {
@@ -38,54 +41,170 @@ __device__ __forceinline__ f32x4 block_sums(i32x8 x, i32x8 w) {
     return d;
 }
 
-// 32 values from p on, of which n are there (the others 0).
-__device__ __forceinline__ i32x8 load32(const uint8_t* p, int64_t n) {
+// A lane's 32 values of the block at p, of which `left` bytes are there: the pieces of 16 at 16 g and 64 + 16 g (four
+// lanes of a row read 64 bytes side by side). What is not there is 0.
+__device__ __forceinline__ i32x8 load_block32(const uint8_t* p, int g, int64_t left) {
     u32x4a lo = u32x4a{0u, 0u, 0u, 0u}, hi = lo;
-    if (n >= 32) {
-        const u32x4b a = *reinterpret_cast<const u32x4b*>(p), b = *reinterpret_cast<const u32x4b*>(p + 16);
+    if (left >= kBlock) {
+        const u32x4b a = *reinterpret_cast<const u32x4b*>(p + 16 * g), b = *reinterpret_cast<const u32x4b*>(p + 64 + 16 * g);
         lo = u32x4a{a.x, a.y, a.z, a.w};
         hi = u32x4a{b.x, b.y, b.z, b.w};
     } else {
         for (int i = 0; i < 16; ++i) {
-            if (i < n) lo[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-            if (16 + i < n) hi[i >> 2] |= (uint32_t)p[16 + i] << (8 * (i & 3));
+            if (16 * g + i < left) lo[i >> 2] |= (uint32_t)p[16 * g + i] << (8 * (i & 3));
+            if (64 + 16 * g + i < left) hi[i >> 2] |= (uint32_t)p[64 + 16 * g + i] << (8 * (i & 3));
         }
     }
     return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-constexpr int kWaves = 4;
+// ---- few rows ---------------------------------------------------------------------------------------
+//
+// 16 MT x 16 NT outputs a workgroup, whose waves take the blocks of K in turn, each straight from memory (x from L2)
+// into operands, two blocks ahead; no wave waits for another before their sums meet in LDS. The scales of x are
+// in LDS from the start. With TAIL the last block of K is not whole.
 
-// 16 x 16 outputs a workgroup, its waves taking the blocks of K in turn.
-__global__ __launch_bounds__(64 * kWaves) void qmm_small_kernel(BlockQmmArgs a) {
-    __shared__ f32x4 red[kWaves][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * 16;
-    const int64_t kb = (a.k + kBlock - 1) / kBlock;
-    const uint8_t* xp = a.x + min(m0 + r, a.m - 1) * a.k + 32 * g;
-    const uint8_t* wp = a.w + min(n0 + r, a.n - 1) * a.k + 32 * g;
-    const float* ws = a.w_scales + n0 / kBlock * kb;
-    const float* xs[4];
+constexpr int kFewWaves = 8;
+
+inline int few_lds(int mt, int nt, int64_t kb) {
+    return (int)std::max((int64_t)mt * 16 * 4 * kb, (int64_t)kFewWaves * mt * nt * 64 * 16);
+}
+constexpr int kFewMaxLds = 152 * 1024;
+
+template <int MT, int NT, bool TAIL>
+__global__ __launch_bounds__(64 * kFewWaves) void qmm_few_kernel(BlockQmmArgs a) {
+    extern __shared__ __attribute__((aligned(16))) float lds[];  // scales [kb][16 MT], then sums [wave][tile][lane][4]
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int kb = (int)((a.k + kBlock - 1) / kBlock), whole = (int)(a.k / kBlock);
+    const uint8_t *xp[MT], *wp[NT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) xs[v] = a.x_scales + min(m0 + 4 * g + v, a.m - 1) * kb;
-    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t j = wave; j < kb; j += kWaves) {
-        const int64_t left = a.k - j * kBlock - 32 * g;
-        const f32x4 d = block_sums(load32(xp + j * kBlock, left), load32(wp + j * kBlock, left));
-        const float s = ws[j];
+    for (int i = 0; i < MT; ++i) xp[i] = a.x + min(m0 + 16 * i + r16, a.m - 1) * a.k;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(xs[v][j] * s, d[v], acc[v]);
+    for (int j = 0; j < NT; ++j) wp[j] = a.w + min(n0 + 16 * j + r16, a.n - 1) * a.k;
+    const float* ws = a.w_scales + n0 / kBlock * kb;  // NT tiles lie in one block of 128 columns
+
+    struct Ahead {
+        i32x8 x[MT], w[NT];
+        float s;
+    };
+    // Each workgroup begins at another block of K: rows 4 KB apart share a channel of L2 block by block, and with all
+    // workgroups at the same one loads take longer ([1, 4096] x [4096, 4096]: 5.5 us against
+    // 6.6, [61, 4096] x [14336, 4096]: 30.5 against 35.5).
+    const int first = whole > 0 ? (int)((uint32_t)blockIdx.x * 5u % (uint32_t)whole) : 0;
+    auto block_of = [&](int b) {
+        const int at = wave + b * kFewWaves + first;
+        return at < whole ? at : at - whole;
+    };
+    auto load = [&](Ahead& s, int, int b) {
+        const int64_t at = (int64_t)block_of(b) * kBlock;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s.w[j] = load_block32(wp[j] + at, g, kBlock);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) s.x[i] = load_block32(xp[i] + at, g, kBlock);
+        s.s = ws[block_of(b)];
+    };
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto products = [&](const Ahead& s, int block) {
+        f16x8 w[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[j][q] = half8(s.w[j], q);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            f32x4 d[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) d[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f16x8 x = half8(s.x[i], q);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) d[j] = mfma16x16x32<true>(x, w[j][q], d[j]);
+            }
+            f32x4 scale = *reinterpret_cast<const f32x4*>(lds + block * (16 * MT) + 16 * i + 4 * g);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) scale[v] *= s.s;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(scale[v], d[j][v], acc[i][j][v]);
+        }
+    };
+    const int items = (whole - wave + kFewWaves - 1) / kFewWaves;
+    Ahead A, B;
+    if (items > 0) {
+        load(A, 0, 0);
+        load(B, 0, min(1, items - 1));
     }
-    red[wave][lane] = acc;
+    for (int i = tid; i < 16 * MT * kb; i += 64 * kFewWaves) {  // rows follow each other: whole rows are read
+        const int row = i / kb, b = i % kb;
+        lds[b * (16 * MT) + row] = a.x_scales[min(m0 + row, a.m - 1) * kb + b];
+    }
     __syncthreads();
-    if (wave) return;
+    if (items > 0)
+        pipeline(items, items, A, B, load, [&](const Ahead& s, int, int b) { products(s, block_of(b)); });
+    if constexpr (TAIL) {
+        if (whole % kFewWaves == wave) {
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) acc += red[w][lane];
-    if (n0 + r >= a.n) return;
+            for (int j = 0; j < NT; ++j) A.w[j] = load_block32(wp[j] + (int64_t)whole * kBlock, g, a.k % kBlock);
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-        if (m0 + 4 * g + v < a.m) store_from_f32(a.y, (size_t)((m0 + 4 * g + v) * a.n + n0 + r), a.dtype, acc[v]);
+            for (int i = 0; i < MT; ++i) A.x[i] = load_block32(xp[i] + (int64_t)whole * kBlock, g, a.k % kBlock);
+            A.s = ws[whole];
+            products(A, whole);
+        }
+    }
+    __syncthreads();  // nobody reads scales any more
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) red[((wave * MT + i) * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int t = wave; t < MT * NT; t += kFewWaves) {
+        f32x4 sum = red[t * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) sum += red[(w * MT * NT + t) * 64 + lane];
+        const int64_t n = n0 + t % NT * 16 + r16;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int64_t m = m0 + t / NT * 16 + 4 * g + v;
+            if (m < a.m && n < a.n) store_from_f32(a.y, (size_t)(m * a.n + n), a.dtype, sum[v]);
+        }
+    }
+}
+
+template <int MT, int NT>
+hipError_t launch_few(const BlockQmmArgs& a, hipStream_t stream) {
+    const int64_t kb = (a.k + kBlock - 1) / kBlock, rows = (int64_t)65535 * 16 * MT;  // a grid's second axis
+    for (int64_t m0 = 0; m0 < a.m; m0 += rows) {
+        BlockQmmArgs p = a;
+        p.m = std::min(rows, a.m - m0);
+        p.x += m0 * a.k;
+        p.x_scales += m0 * kb;
+        p.y = static_cast<char*>(a.y) + m0 * a.n * (a.dtype == 0 ? 4 : 2);
+        const dim3 grid((unsigned)((a.n + 16 * NT - 1) / (16 * NT)), (unsigned)((p.m + 16 * MT - 1) / (16 * MT)));
+        if (a.k % kBlock) qmm_few_kernel<MT, NT, true><<<grid, dim3(64 * kFewWaves), few_lds(MT, NT, kb), stream>>>(p);
+        else qmm_few_kernel<MT, NT, false><<<grid, dim3(64 * kFewWaves), few_lds(MT, NT, kb), stream>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// Columns a workgroup: 64, 32 or 16, the most that still give every compute unit one.
+template <int MT>
+hipError_t launch_few_rows(const BlockQmmArgs& a, hipStream_t stream) {
+    const int64_t tiles = ((a.m + 16 * MT - 1) / (16 * MT)) * ((a.n + 15) / 16), cus = device_cu_count();
+    if (tiles >= 4 * cus) return launch_few<MT, 4>(a, stream);
+    if (tiles >= 2 * cus) return launch_few<MT, 2>(a, stream);
+    return launch_few<MT, 1>(a, stream);
 }
 
 // ---- tiles -----------------------------------------------------------------------------------------
@@ -321,18 +440,10 @@ hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t stream) {
         if (big >= device_cu_count() * 3 / 4) return launch_tiles<8, 8, 2>(a, stream);
         return launch_tiles<4, 4, 2>(a, stream);
     }
-    const int64_t rows = 65535 * 16;  // a grid's second axis
-    for (int64_t m0 = 0; m0 < a.m; m0 += rows) {
-        BlockQmmArgs p = a;
-        p.m = a.m - m0 < rows ? a.m - m0 : rows;
-        p.x += m0 * a.k;
-        p.x_scales += m0 * ((a.k + kBlock - 1) / kBlock);
-        p.y = static_cast<char*>(a.y) + m0 * a.n * (a.dtype == 0 ? 4 : 2);
-        qmm_small_kernel<<<dim3((unsigned)((a.n + 15) / 16), (unsigned)((p.m + 15) / 16)), dim3(64 * kWaves), 0, stream>>>(p);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const int64_t kb = (a.k + kBlock - 1) / kBlock;
+    if (a.m > 32 && few_lds(4, 4, kb) <= kFewMaxLds) return launch_few_rows<4>(a, stream);
+    if (a.m > 16 && few_lds(2, 4, kb) <= kFewMaxLds) return launch_few_rows<2>(a, stream);
+    return launch_few_rows<1>(a, stream);
 }
 
 }  // namespace qaff

@@ -170,22 +170,37 @@ template <int WORDS> __device__ __forceinline__ void load_halves(const uint16_t*
     }
 }
 
-// Unit u of weight row `row` (counted over all experts, of `all` rows). The blocks past the row's end repeat its
-// last one (x is 0 there); the groups past it are the next row's, and are masked where they are used.
+// One expert's part of a weight: rows of kb blocks, and how many halves of scales lie from its first on to the end of
+// the tensor (at most 2^31 - 1 of them matter).
+struct ExpertRows {
+    const uint32_t* packed;
+    const uint16_t *scales, *biases;
+    int kb, halves;
+};
 template <int BITS, int GSHIFT>
-__device__ __forceinline__ void load_unit(UnitLoads<BITS, GSHIFT>& L, const ExpertWeight& W, int64_t row, int64_t all, int u,
-                                          int kb, int g) {
+__device__ __forceinline__ ExpertRows expert_rows(const ExpertWeight& W, int e, int experts, int n, int kb) {
+    const int64_t gpr = kb >> GSHIFT, row = (int64_t)e * n;
+    const int64_t halves = ((int64_t)experts * n - row) * gpr;
+    return ExpertRows{W.packed + row * kb * BITS, W.scales + row * gpr, W.biases + row * gpr, kb,
+                      (int)(halves < 0x7fffffff ? halves : 0x7fffffff)};
+}
+
+// Unit u of row `row` (an expert's codes and groups are counted in 32 bits: 2^15 rows of 2^15 codes at most). The blocks
+// past the row's end repeat its last one (x is 0 there); the groups past it are the next row's, and are masked where
+// they are used.
+template <int BITS, int GSHIFT>
+__device__ __forceinline__ void load_unit(UnitLoads<BITS, GSHIFT>& L, const ExpertRows& W, int row, int u, int g) {
     typedef UnitLoads<BITS, GSHIFT> U;
-    const int gpr = kb >> GSHIFT;
-    const int64_t want = row * gpr + u * U::kGroups, last = all * gpr - 2 * U::kWords;  // a tensor has 32 rows at least
-    const int64_t at = want < last ? want : last;
-    L.over = (int)(want - at);
-    load_halves(W.scales + at, L.s);
-    load_halves(W.biases + at, L.b);
-    const uint32_t* pw = W.packed + row * kb * BITS;
+    const int want = row * (W.kb >> GSHIFT) + u * U::kGroups;
+    const int at = min(want, W.halves - 2 * U::kWords);  // a tensor has 32 rows at least
+    L.over = want - at;
+    load_halves(W.scales + (uint32_t)at, L.s);
+    load_halves(W.biases + (uint32_t)at, L.b);
 #pragma unroll
-    for (int c = 0; c < kUnit<BITS>; ++c)
-        load_block<BITS>(pw + min(4 * (u * kUnit<BITS> + c) + g, kb - 1) * BITS, L.w[c]);
+    for (int c = 0; c < kUnit<BITS>; ++c) {
+        const uint32_t block = (uint32_t)(row * W.kb + min(4 * (u * kUnit<BITS> + c) + g, W.kb - 1));
+        load_block<BITS>(W.packed + block * BITS, L.w[c]);
+    }
 }
 
 // The window of a row's last unit, which `there` groups of it fill, moved to its place and masked.
@@ -272,37 +287,6 @@ __device__ __forceinline__ void stage_octet(u32x4h h, bool there, int o, uint8_t
     *reinterpret_cast<u32x4a*>(xl + 16 * o) = v;
 }
 
-// Walks items (turn, i), 0 <= i < each, in order, with the next two in the registers A and B (which hold the first two
-// at the start). The loads in the loop have no conditions: the compiler counts those on their way to wait for the ones
-// it needs, and with a branch around some would wait for all. So the last one may repeat an item that is there.
-template <typename Units, typename Load, typename Take>
-__device__ __forceinline__ void pipeline(int items, int each, Units& A, Units& B, Load load, Take take) {
-    int t0 = 0, i0 = 0, t1 = 0, i1 = 0;  // the items in A and B
-    auto advance = [&](int& t, int& i) {
-        if (++i >= each) {
-            i = 0;
-            ++t;
-        }
-    };
-    advance(t1, i1);
-    int n = 0;
-    for (; n + 2 < items; n += 2) {
-        int t = t1, i = i1;
-        advance(t, i);
-        take(A, t0, i0);
-        load(A, t, i);
-        t0 = t;
-        i0 = i;
-        if (n + 3 < items) advance(t, i);
-        take(B, t1, i1);
-        load(B, t, i);
-        t1 = t;
-        i1 = i;
-    }
-    take(A, t0, i0);
-    if (n + 1 < items) take(B, t1, i1);
-}
-
 // Pairs of expert e whose rank lies in [first, first + count) into rows[0 ..), by the whole workgroup; returns how
 // many the expert has, up to that point or more. Eight pairs a thread at a time, all of them loaded together;
 // counts: LDS for the hits of each 64 of them.
@@ -372,14 +356,14 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_few_kernel(FewArg
     const int turns = (tiles - (int)blockIdx.x * side + step - 1) / step;  // the same for all waves
 
     typedef UnitLoads<BITS, GSHIFT> Unit;
+    const ExpertRows w0 = expert_rows<BITS, GSHIFT>(a.w0, e, a.experts, a.n, kb);
+    const ExpertRows w1 = expert_rows<BITS, GSHIFT>(a.w1, e, a.experts, a.n, kb);
     // Item (turn, i): unit u0 + i of tile t0 + turn step. Items past the row's end or the last tile repeat others.
     auto load = [&](Unit (&L)[2], int turn, int i) {
         const int n0 = min(t0 + turn * step, tiles - 1) * kTileN + r16;
-        const int64_t row0 = (int64_t)e * a.n + min(n0, a.n - 1);
-        const int64_t row1 = DOWN ? (int64_t)e * a.n + min(n0 + 16, a.n - 1) : row0;
         const int u = min(u0 + i, units - 1);
-        load_unit(L[0], a.w0, row0, (int64_t)a.experts * a.n, u, kb, g);
-        load_unit(L[1], DOWN ? a.w0 : a.w1, row1, (int64_t)a.experts * a.n, u, kb, g);
+        load_unit(L[0], w0, min(n0, a.n - 1), u, g);
+        load_unit(L[1], DOWN ? w0 : w1, min(DOWN ? n0 + 16 : n0, a.n - 1), u, g);
     };
     Unit A[2], B[2];
     const CodeConsts cc = make_code_consts<F16>();
@@ -494,19 +478,20 @@ __global__ __launch_bounds__(kFewThreads, kFewBlocks) void moe_pair_kernel(FewAr
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int64_t p = blockIdx.y;
-    const int e = a.chosen[p];
+    const int e = __builtin_amdgcn_readfirstlane(a.chosen[p]);
     if ((uint32_t)e >= (uint32_t)a.experts) return;
     uint8_t* xl = smem;
     float* xs = reinterpret_cast<float*>(smem + 2 * a.kpad);
     const int kb = a.k / 32, units = a.kpad / (128 * kUnit<BITS>), each = (units + kFewWaves - 1) / kFewWaves;
     const int u0 = wave * each;
     typedef UnitLoads<BITS, GSHIFT> Unit;
-    const int n0 = blockIdx.x * 16 + r16;
-    const int64_t row = (int64_t)e * a.n + min(n0, a.n - 1), all = (int64_t)a.experts * a.n;
+    const int n0 = blockIdx.x * 16 + r16, row = min(n0, a.n - 1);
+    const ExpertRows w0 = expert_rows<BITS, GSHIFT>(a.w0, e, a.experts, a.n, kb);
+    const ExpertRows w1 = expert_rows<BITS, GSHIFT>(a.w1, e, a.experts, a.n, kb);
     auto load = [&](Unit (&L)[2], int, int i) {
         const int u = min(u0 + i, units - 1);
-        load_unit(L[0], a.w0, row, all, u, kb, g);
-        load_unit(L[1], a.w1, row, all, u, kb, g);
+        load_unit(L[0], w0, row, u, g);
+        load_unit(L[1], w1, row, u, g);
     };
     Unit A[2], B[2];
     const CodeConsts cc = make_code_consts<F16>();
@@ -560,10 +545,9 @@ __global__ __launch_bounds__(64 * kPairWaves) void moe_pair_down_kernel(FewArgs 
         const int64_t p = t * a.top_k + min(j, a.top_k - 1);
         const int e = __builtin_amdgcn_readfirstlane(a.chosen[p]);
         const bool there = j < a.top_k && (uint32_t)e < (uint32_t)a.experts;
-        const int64_t all = (int64_t)a.experts * a.n;
-        const int64_t row = (int64_t)(there ? e : 0) * a.n + min(n0, a.n - 1);
+        const ExpertRows w0 = expert_rows<BITS, GSHIFT>(a.w0, there ? e : 0, a.experts, a.n, kb);
         const int u0 = (wave & 1) * each, mine = there ? min(each, units - u0) : 0;
-        auto load = [&](Unit& L, int, int i) { load_unit(L, a.w0, row, all, min(u0 + i, units - 1), kb, g); };
+        auto load = [&](Unit& L, int, int i) { load_unit(L, w0, min(n0, a.n - 1), min(u0 + i, units - 1), g); };
         Unit A, B;
         if (mine > 0) load(A, 0, 0);
         if (mine > 1) load(B, 0, 1);
@@ -647,7 +631,7 @@ hipError_t launch_few_kernel(FewArgs a, hipStream_t stream) {
     // Rows of x a pass: 16, or 8 up to an average of 4 rows an expert that is used (a smaller x lets more workgroups
     // share a compute unit: 16 rows of 2048 values two, 8 rows three).
     const int64_t used = std::min(a.pairs, (int64_t)a.experts);
-    a.rows = (int)std::min(a.pairs, a.pairs <= 4 * used ? (int64_t)8 : (int64_t)kTileRows);
+    a.rows = (int)std::min(a.pairs, a.pairs <= 2 * used ? (int64_t)8 : (int64_t)kTileRows);
     while (a.rows > 1 && a.rows * pitch + sums + kRed > 150 * 1024) a.rows = (a.rows + 1) / 2;
     const int lds = a.rows * pitch + sums + kRed;
     const int tiles = (a.n + (DOWN ? 31 : 15)) / (DOWN ? 32 : 16);

@@ -1,4 +1,5 @@
-// Sums over a wave's 64 lanes in registers (DPP), without LDS round trips.
+// Sums over a wave's 64 lanes in registers (DPP), without LDS round trips, and a stream of loads that stays ahead of
+// their use.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,5 +30,36 @@ template <typename T> __device__ __forceinline__ T wave_scan(T v) {
 
 // Lane `lane`'s value (the same lane for the whole wave), in a scalar register.
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Walks items (turn, i), 0 <= i < each, in order, with the next two in the registers A and B (which hold the first two
+// at the start). The loads in the loop have no conditions: the compiler counts those on their way to wait for the ones
+// it needs, and with a branch around some would wait for all. So the last one may repeat an item that is there.
+template <typename Units, typename Load, typename Take>
+__device__ __forceinline__ void pipeline(int items, int each, Units& A, Units& B, Load load, Take take) {
+    int t0 = 0, i0 = 0, t1 = 0, i1 = 0;  // the items in A and B
+    auto advance = [&](int& t, int& i) {
+        if (++i >= each) {
+            i = 0;
+            ++t;
+        }
+    };
+    advance(t1, i1);
+    int n = 0;
+    for (; n + 2 < items; n += 2) {
+        int t = t1, i = i1;
+        advance(t, i);
+        take(A, t0, i0);
+        load(A, t, i);
+        t0 = t;
+        i0 = i;
+        if (n + 3 < items) advance(t, i);
+        take(B, t1, i1);
+        load(B, t, i);
+        t1 = t;
+        i1 = i;
+    }
+    take(A, t0, i0);
+    if (n + 1 < items) take(B, t1, i1);
+}
 
 }  // namespace qaff
