@@ -49,9 +49,10 @@ hipError_t launch_moe_ffn(const MoeArgs& a, bool f16, hipStream_t stream);
 // Bytes of workspace for these sizes.
 size_t moe_ffn_workspace(int64_t tokens, int64_t width, int64_t hidden, int64_t top_k, int64_t experts);
 
-// The format's two halves (one translation unit each).
-hipError_t launch_moe_ffn_bf16(const MoeArgs& a, hipStream_t stream);
-hipError_t launch_moe_ffn_f16(const MoeArgs& a, hipStream_t stream);
+// Its kernels: few rows an expert (one translation unit a type), and many.
+hipError_t launch_moe_few_bf16(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_few_f16(const MoeArgs& a, hipStream_t stream);
+hipError_t launch_moe_many(const MoeArgs& a, bool f16, hipStream_t stream);
 
 constexpr int kBlock = 128;  // columns (and, for weights, rows) that share a scale
 

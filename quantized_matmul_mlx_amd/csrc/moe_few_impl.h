@@ -717,5 +717,19 @@ hipError_t launch_few_bits(const MoeArgs& a, hipStream_t stream) {
     return launch_few<BITS, 2, F16>(a, stream);
 }
 
+template <bool F16>
+hipError_t launch_few_any(const MoeArgs& a, hipStream_t stream) {
+    switch (a.bits) {
+        case 1: return launch_few_bits<1, F16>(a, stream);
+        case 2: return launch_few_bits<2, F16>(a, stream);
+        case 3: return launch_few_bits<3, F16>(a, stream);
+        case 4: return launch_few_bits<4, F16>(a, stream);
+        case 5: return launch_few_bits<5, F16>(a, stream);
+        case 6: return launch_few_bits<6, F16>(a, stream);
+        case 8: return launch_few_bits<8, F16>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
 }  // namespace
 }  // namespace qaff

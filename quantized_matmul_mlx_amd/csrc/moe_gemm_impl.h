@@ -33,31 +33,51 @@ constexpr int kTileM = 32 * kMT;       // rows
 constexpr int kGemmThreads = 256;
 constexpr int kStep = 64;              // codes a stage of x
 constexpr int kPitch = 2 * kStep;      // bytes of a row of a stage
-constexpr int kPieceCount = kTileM * 8 / kGemmThreads;  // 16-byte pieces of a stage a thread
 
 struct GemmArgs {
     const uint16_t* x;       // float16 rows of k values: [tokens] (DOWN false) or [sorted pairs]
     const float* x_scale;    // [tokens] what a row of x was divided by, or null
-    const int8_t* h_exp;     // [sorted pairs, hidden / 16] exponents of h
+    int8_t* h_exp;           // [sorted pairs, hidden / 16] exponents of h
+    int32_t* h_most;         // [sorted pairs] the largest of them, + 128
     ExpertWeight w0, w1;
     const int32_t* order;    // [pairs]: sorted position -> pair
     const int32_t* offsets;  // [experts + 1]
     const float* weights;    // [pairs]
     uint16_t* h;             // [sorted pairs, n]
-    int8_t* h_exp_out;
     float* d;                // [pairs, n]
-    int k, n, top_k, experts, tiles_n, blocks;
+    int k, n, top_k, experts, tiles_n;
+    int gshift;              // group size 32 << gshift
+    int f16;                 // type of scales and biases
 };
 
 // ---- the order of the pairs, and x as float16 -----------------------------------------------------
 
 constexpr int kSortThreads = 1024;
 
+// Four pairs' experts from p on; -1 past the last pair.
+__device__ __forceinline__ void sort_load(const int32_t* chosen, int64_t pairs, int64_t p, int (&c)[4]) {
+    const int64_t at = min(p, max(pairs - 4, (int64_t)0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = chosen[min(at + i, pairs - 1)];
+    if (p + 4 > pairs) {  // the loads above began early
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = p + i < pairs ? chosen[p + i] : -1;
+    }
+}
+__device__ __forceinline__ int sort_less(const int32_t* chosen, int64_t pairs, int64_t p, int e) {
+    int c[4], n = 0;
+    sort_load(chosen, pairs, p, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += c[i] >= 0 && c[i] < e;
+    return n;
+}
+
 // Workgroup e < experts: offsets[e] = pairs of lower experts, order[offsets[e] ..] = its pairs. The others: rows
 // of x, a wave each, divided by a power of two that puts the largest value into [2^14, 2^15).
 __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* chosen, int64_t pairs, int experts,
                                                                 int32_t* order, int32_t* offsets, const uint16_t* x,
-                                                                int64_t tokens, int width, uint16_t* xh, float* x_scale) {
+                                                                int64_t tokens, int width, uint16_t* xh, float* x_scale,
+                                                                int32_t* h_most) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if ((int)blockIdx.x >= experts) {
         const int64_t t = (int64_t)(blockIdx.x - experts) * (kSortThreads / 64) + wave;
@@ -85,32 +105,48 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* c
         if (lane == 0) x_scale[t] = ldexpf(1.f, -up);
         return;
     }
-    __shared__ int sums[2][kSortThreads / 64];
+    // Four runs of 4 pairs a thread at a time: run, thread and place order the pairs.
+    constexpr int kWaves = kSortThreads / 64, kRuns = 4;
+    __shared__ uint32_t sums[kRuns * kWaves];
     const int e = blockIdx.x;
-    // a thread's pairs lie side by side, so that its rank orders them
-    const int64_t each = (pairs + kSortThreads - 1) / kSortThreads;
-    const int64_t p0 = tid * each, p1 = min(pairs, p0 + each);
-    int less = 0, mine = 0;
-    for (int64_t p = p0; p < p1; ++p) {
-        const int c = chosen[p];
-        less += c >= 0 && c < e;
-        mine += c == e;
-    }
-    const int before = wave_scan(mine);
-    const int lower = wave_scan(less);
-    if (lane == 63) {
-        sums[0][wave] = before;
-        sums[1][wave] = lower;
-    }
+    int base = 0;
+    for (int64_t p0 = 0; p0 < pairs; p0 += 4 * kSortThreads) base += sort_less(chosen, pairs, p0 + 4 * tid, e);
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) base += __shfl_xor(base, s, 64);
+    if (lane == 0) sums[wave] = (uint32_t)base;
     __syncthreads();
-    int at = before - mine, base = 0, total = 0;
-    for (int w = 0; w < kSortThreads / 64; ++w) {
-        if (w < wave) at += sums[0][w];
-        total += sums[0][w];
-        base += sums[1][w];
+    base = 0;
+    for (int w = 0; w < kWaves; ++w) base += (int)sums[w];
+    __syncthreads();
+    int total = 0;
+    for (int64_t p0 = 0; p0 < pairs; p0 += 4 * kRuns * kSortThreads) {
+        int c[kRuns][4];
+        uint32_t before[kRuns];
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) sort_load(chosen, pairs, p0 + 4 * (q * kSortThreads + tid), c[q]);
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) {
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine += c[q][i] == e;
+            const int upto = wave_scan(mine);
+            before[q] = upto - mine;
+            if (lane == 63) sums[q * kWaves + wave] = upto;
+        }
+        __syncthreads();
+        const int own = (int)sums[lane];  // kRuns * kWaves = 64 sums
+        const int upto = wave_scan(own);
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) {
+            int at = base + total + (int)before[q] + __shfl(upto - own, q * kWaves + wave, 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c[q][i] == e) order[at++] = (int)(p0 + 4 * (q * kSortThreads + tid) + i);
+        }
+        total += __shfl(upto, 63, 64);
+        __syncthreads();
     }
-    for (int64_t p = p0; p < p1; ++p)
-        if (chosen[p] == e) order[base + at++] = (int)p;
+    for (int i = tid; i < total; i += kSortThreads) h_most[base + i] = 0;
     if (tid == 0) {
         offsets[e] = base;
         if (e == experts - 1) offsets[experts] = base + total;
@@ -157,11 +193,186 @@ __device__ __forceinline__ f16x8 weight_operand(const uint32_t (&w)[BITS], int j
 inline int gemm_lds_bytes(int k, int group) { return 2 * kTileM * kPitch + 128 * (k / group + 1) * 4; }
 constexpr int kGemmMaxLds = 158 * 1024;
 
-template <int BITS, int GSHIFT, bool F16, bool DOWN>
+// The largest magnitude of the 16 lanes of a row.
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, __int_as_float(dpp<0xB1, 0xf>(__float_as_int(v))));   // lane ^ 1
+    v = fmaxf(v, __int_as_float(dpp<0x4E, 0xf>(__float_as_int(v))));   // lane ^ 2
+    v = fmaxf(v, __int_as_float(dpp<0x141, 0xf>(__float_as_int(v))));  // mirrored in 8
+    return fmaxf(v, __int_as_float(dpp<0x140, 0xf>(__float_as_int(v))));  // and in 16
+}
+
+// What a workgroup finds before its loop.
+struct GemmTile {
+    const uint32_t* pw;      // this lane's weight row
+    uint32_t* sb;            // its scales and biases in LDS
+    uint8_t* xl;
+    const int *src, *pair;   // [kTileM] in LDS
+    const float* row_scale;
+    const int* most;         // DOWN: h_most of the row, + 128
+    float col_scale;
+    int row0, rows, wrow, tn;
+};
+
+// T turns of 32 rows.
+template <int BITS, bool DOWN, int T>
+__device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, int tid) {
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 31, h = lane >> 5;
+    const int kb = a.k / 32, gpr = kb >> a.gshift;
+
+    // This thread's pieces of a stage: row i * 32 + tid / 8, 16 bytes at slot tid % 8. Stage t = 2 u + s holds codes
+    // 128 u + 32 s .. + 31 (k-slot 0) and 128 u + 64 + 32 s .. (k-slot 1).
+    const int piece = tid & 7, col_in = (piece >> 2) * 64 + (piece & 3) * 8;
+    const uint16_t* xp[T];
+    const int8_t* ep[T];
+    int most[T];
+    uint8_t* to[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        const int row = i * 32 + tid / 8;
+        xp[i] = a.x + (int64_t)c.src[row] * a.k;
+        if constexpr (DOWN) {
+            ep[i] = a.h_exp + (int64_t)c.src[row] * (a.k / 16);
+            most[i] = c.most[row] - 128;
+        }
+        to[i] = c.xl + row * kPitch + ((piece ^ (row >> 1)) & 7) * 16;
+    }
+    struct Ahead {
+        u32x4h x[T];
+        int e[T];
+    };
+    auto load_x = [&](Ahead& s, int t) {  // columns past the row's end repeat the last ones
+        const int col = min((t >> 1) * 128 + (t & 1) * 32 + col_in, a.k - 8);
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            s.x[i] = *reinterpret_cast<const u32x4h*>(xp[i] + col);
+            if constexpr (DOWN) s.e[i] = ep[i][col / 16];
+        }
+    };
+    auto store_x = [&](const Ahead& s, int t) {
+        const bool there = (t >> 1) * 128 + (t & 1) * 32 + col_in < a.k;
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            u32x4a v = u32x4a{s.x[i].x, s.x[i].y, s.x[i].z, s.x[i].w};
+            if constexpr (DOWN) {  // to the power of two of the row: 2^(e - most), at least 2^-40 (0 in float16)
+                const _Float16 f = (_Float16)__int_as_float((max(s.e[i] - most[i], -40) + 127) << 23);
+                const h2 f2 = {f, f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (uint32_t)v[q]) * f2);
+            }
+            if constexpr (BITS == 4)
+                v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                           __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = there ? v[q] : 0u;
+            *reinterpret_cast<u32x4a*>(to[i] + (t & 1) * (kTileM * kPitch)) = v;
+        }
+    };
+    // A unit of 128 codes: this lane's blocks 2 h and 2 h + 1 of its four.
+    const int units = (a.k + 127) / 128;
+    auto load_w = [&](uint32_t (&w)[2][BITS], int u) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) load_block<BITS>(c.pw + min(4 * min(u, units - 1) + 2 * h + s, kb - 1) * BITS, w[s]);
+    };
+    f32x16 acc[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
+    auto products = [&](const uint32_t (&w)[BITS], int t) {
+        const uint8_t* from = c.xl + (t & 1) * (kTileM * kPitch) + r * kPitch;
+        const uint32_t g = c.sb[min(((t >> 1) * 4 + 2 * h + (t & 1)) >> a.gshift, gpr - 1)];
+        uint32_t own[BITS];
+#pragma unroll
+        for (int i = 0; i < BITS; ++i) {
+            own[i] = w[i];
+            asm volatile("" : "+v"(own[i]));  // here, not where the loads are issued, which would wait for them
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f16x8 o = weight_operand<BITS>(own, q, g);
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+                acc[i] = mfma32x32x16<true>(
+                    *reinterpret_cast<const f16x8*>(from + i * 32 * kPitch + ((4 * h + q) ^ (r >> 1 & 7)) * 16), o, acc[i]);
+        }
+    };
+
+    // x: a stage in LDS while one is multiplied, two more in registers. Weights: a unit and two more.
+    const int stages = 2 * units;
+    Ahead xa, xb;
+    uint32_t w0[2][BITS], w1[2][BITS], w2[2][BITS];
+    load_x(xa, 0);
+    load_w(w0, 0);
+    load_x(xb, 1);
+    load_w(w1, 1);
+    store_x(xa, 0);
+    load_x(xa, 2);
+    auto unit = [&](int u, const uint32_t (&w)[2][BITS], uint32_t (&next)[2][BITS]) {
+        const int t = 2 * u;
+        __syncthreads();  // stage t is there; nobody reads the other place any more
+        store_x(xb, t + 1);
+        load_x(xb, t + 3);
+        load_w(next, u + 2);
+        products(w[0], t);
+        __syncthreads();
+        store_x(xa, t + 2);
+        load_x(xa, t + 4);
+        products(w[1], t + 1);
+    };
+    for (int u = 0;; u += 3) {
+        unit(u, w0, w2);
+        if (u + 1 >= units) break;
+        unit(u + 1, w1, w0);
+        if (u + 2 >= units) break;
+        unit(u + 2, w2, w1);
+        if (u + 3 >= units) break;
+    }
+    (void)stages;
+
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        if constexpr (DOWN) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+                if (row < c.rows && c.wrow < a.n)
+                    a.d[(int64_t)c.pair[row] * a.n + c.wrow] = acc[i][v] * (c.row_scale[row] * c.col_scale);
+            }
+        } else {
+            // lanes r < 16 hold gate and r >= 16 up results: exchanged in pairs of rows, lanes with r < 16 keep row v
+            // and the others row v + 1
+            const float other = __shfl_xor(c.col_scale, 16, 64);
+            const float gs = r < 16 ? c.col_scale : other, us = r < 16 ? other : c.col_scale;
+#pragma unroll
+            for (int v = 0; v < 16; v += 2) {
+                uint32_t x0 = __float_as_uint(acc[i][v]), x1 = __float_as_uint(acc[i][v + 1]);
+                swap16(x0, x1);
+                const int vv = v + (r >> 4);
+                const int row = 32 * i + 8 * (vv >> 2) + 4 * h + (vv & 3);
+                const float xs = c.row_scale[row];
+                const float hv = silu_f32(__uint_as_float(x0) * gs * xs) * (__uint_as_float(x1) * us * xs);
+                // the power of two of the row's 16 columns
+                const int ex = min(max((int)(__float_as_uint(row_max(fabsf(hv))) >> 23), 1), 254) - 127;
+                if (row < c.rows && 64 * c.tn + 16 * wave < a.n) {
+                    const int64_t at = c.row0 + row;
+                    a.h[at * a.n + c.wrow] = f32_to_half_bits<true>(ldexpf(hv, -ex));
+                    if ((r & 15) == 0) {
+                        a.h_exp[at * (a.n / 16) + (64 * c.tn + 16 * wave) / 16] = (int8_t)ex;
+                        atomicMax(a.h_most + at, ex + 128);  // the order does not matter
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <int BITS, bool DOWN>
 __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     __shared__ int src[kTileM];        // row of x
     __shared__ int pair[kTileM];       // DOWN: pair of the row
+    __shared__ int most[kTileM];
     __shared__ float row_scale[kTileM];
     __shared__ int where[3];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -181,8 +392,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
             const int upto = first + wave_scan(tiles);
             const uint64_t past = __builtin_amdgcn_ballot_w64(upto > tile);
             if (past) {
-                found = base + __builtin_ctzll(past);
                 const int l = __builtin_ctzll(past);
+                found = base + l;
                 first = __shfl(upto - tiles, l, 64);
             } else {
                 first = __shfl(upto, 63, 64);
@@ -199,191 +410,65 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     __syncthreads();
     const int e = where[0];
     if (e < 0) return;
-    const int row0 = where[1], rows = min(kTileM, where[2] - row0);
-    const int turns = (rows + 31) / 32;
-    const int kb = a.k / 32, gpr = kb >> GSHIFT, spitch = gpr + 1;
-    uint8_t* xl = smem;
-    uint32_t* sb = reinterpret_cast<uint32_t*>(smem + 2 * kTileM * kPitch);
-
-    // this wave's weight rows: gate rows 64 tn + 16 wave + r and the up rows of the same columns, or 128 tn + ...
-    const int wrow = DOWN ? 128 * tn + 32 * wave + r : 64 * tn + 16 * wave + (r & 15);
-    const ExpertWeight& W = !DOWN && r >= 16 ? a.w1 : a.w0;
-    const int64_t wr = (int64_t)e * a.n + min(wrow, a.n - 1);
-    const uint32_t* pw = W.packed + wr * kb * BITS;
-
-    // scales and biases to LDS, times the power of two of the row: the largest scale 2^24 lies in [2^14, 2^15)
-    const uint16_t* sp = W.scales + wr * gpr;
-    const uint16_t* bp = W.biases + wr * gpr;
-    float top = 0.f;
-    for (int g = h; g < gpr; g += 2)
-        top = fmaxf(top, fmaxf(fabsf(half_to_f32<F16>(sp[g])), fabsf(half_to_f32<F16>(bp[g])) * 0x1p-20f));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const int up = min(14 + 127 - max(min((int)(__float_as_uint(top) >> 23), 254), 1), 120);
-    uint32_t* sbw = sb + (32 * wave + r) * spitch;
-    for (int g = h; g < gpr; g += 2)
-        sbw[g] = pack_half2<true>(ldexpf(half_to_f32<F16>(sp[g]), up), ldexpf(half_to_f32<F16>(bp[g]), up - 24));
-    const float col_scale = ldexpf(1.f, 24 - up);
+    GemmTile c;
+    c.row0 = where[1];
+    c.rows = min(kTileM, where[2] - c.row0);
+    c.tn = tn;
+    const int kb = a.k / 32, gpr = kb >> a.gshift, spitch = gpr + 1;
 
     // rows of x: where they are and their power of two
     for (int i = tid; i < kTileM; i += kGemmThreads) {
-        const int at = row0 + min(i, rows - 1);
+        const int at = c.row0 + min(i, c.rows - 1);
         const int p = a.order[at];
         if constexpr (DOWN) {
+            const int m = a.h_most[at];
             src[i] = at;
             pair[i] = p;
-            int most = -128;
-            for (int c = 0; c < a.k / 16; ++c) most = max(most, (int)a.h_exp[(int64_t)at * (a.k / 16) + c]);
-            row_scale[i] = __int_as_float(most);  // the exponent, for now
+            most[i] = m;
+            row_scale[i] = a.weights[p] * ldexpf(1.f, m - 128);
         } else {
             src[i] = p / a.top_k;
             row_scale[i] = a.x_scale ? a.x_scale[p / a.top_k] : 1.f;
         }
     }
+
+    // this wave's weight rows: gate rows 64 tn + 16 wave + r and the up rows of the same columns, or 128 tn + ...
+    c.wrow = DOWN ? 128 * tn + 32 * wave + r : 64 * tn + 16 * wave + (r & 15);
+    const ExpertWeight& W = !DOWN && r >= 16 ? a.w1 : a.w0;
+    const int64_t wr = (int64_t)e * a.n + min(c.wrow, a.n - 1);
+    c.pw = W.packed + wr * kb * BITS;
+
+    // scales and biases to LDS, times the power of two of the row: the largest scale 2^24 lies in [2^14, 2^15)
+    const uint16_t* sp = W.scales + wr * gpr;
+    const uint16_t* bp = W.biases + wr * gpr;
+    auto value = [&](uint16_t v) { return a.f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
+    float top = 0.f;
+#pragma unroll 8
+    for (int g = h; g < gpr; g += 2) top = fmaxf(top, fmaxf(fabsf(value(sp[g])), fabsf(value(bp[g])) * 0x1p-20f));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const int up = min(14 + 127 - max(min((int)(__float_as_uint(top) >> 23), 254), 1), 120);
+    c.sb = reinterpret_cast<uint32_t*>(smem + 2 * kTileM * kPitch) + (32 * wave + r) * spitch;
+#pragma unroll 8
+    for (int g = h; g < gpr; g += 2) c.sb[g] = pack_half2<true>(ldexpf(value(sp[g]), up), ldexpf(value(bp[g]), up - 24));
+    c.col_scale = ldexpf(1.f, 24 - up);
+    c.xl = smem;
+    c.src = src;
+    c.pair = pair;
+    c.most = most;
+    c.row_scale = row_scale;
     __syncthreads();
-
-    // this thread's pieces of a stage: row i * 32 + tid / 8, 16 bytes at slot tid % 8. Stage t = 2 u + s holds codes
-    // 128 u + 32 s .. + 31 (k-slot 0) and 128 u + 64 + 32 s .. (k-slot 1).
-    const int piece = tid & 7;
-    const int col_in = (piece >> 2) * 64 + (piece & 3) * 8;
-    const uint16_t* xp[kPieceCount];
-    int most[kPieceCount];
-#pragma unroll
-    for (int i = 0; i < kPieceCount; ++i) {
-        const int row = i * 32 + tid / 8;
-        xp[i] = a.x + (int64_t)src[row] * a.k;
-        if constexpr (DOWN) most[i] = __float_as_int(row_scale[row]);
-    }
-    if constexpr (DOWN) {
-        __syncthreads();
-        for (int i = tid; i < kTileM; i += kGemmThreads)
-            row_scale[i] = a.weights[pair[i]] * ldexpf(1.f, __float_as_int(row_scale[i]));
-    }
-    u32x4a xr[kPieceCount];
-    int xe[kPieceCount];
-    auto load_x = [&](int t) {
-        const int c = (t >> 1) * 128 + (t & 1) * 32 + col_in;
-#pragma unroll
-        for (int i = 0; i < kPieceCount; ++i) {
-            xr[i] = u32x4a{0u, 0u, 0u, 0u};
-            xe[i] = 0;
-            if (i < turns && c < a.k) {
-                const u32x4h v = *reinterpret_cast<const u32x4h*>(xp[i] + c);
-                xr[i] = u32x4a{v.x, v.y, v.z, v.w};
-                if constexpr (DOWN) xe[i] = a.h_exp[(int64_t)src[i * 32 + tid / 8] * (a.k / 16) + c / 16];
-            }
-        }
-    };
-    auto store_x = [&](int t) {
-        uint8_t* to = xl + (t & 1) * (kTileM * kPitch);
-#pragma unroll
-        for (int i = 0; i < kPieceCount; ++i) {
-            if (i >= turns) continue;
-            const int row = i * 32 + tid / 8;
-            u32x4a v = xr[i];
-            if constexpr (DOWN) {  // to the power of two of the row
-                const _Float16 f = (_Float16)ldexpf(1.f, max(xe[i] - most[i], -30));
-                const h2 f2 = {f, f};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (uint32_t)v[q]) * f2);
-            }
-            if constexpr (BITS == 4)
-                v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                           __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-            *reinterpret_cast<u32x4a*>(to + row * kPitch + ((piece ^ (row >> 1)) & 7) * 16) = v;
-        }
-    };
-    // A unit of 128 codes: this lane's blocks 2 h and 2 h + 1 of its four.
-    const int units = (a.k + 127) / 128;
-    uint32_t wq[2][2][BITS];
-    auto load_w = [&](uint32_t (&w)[2][BITS], int u) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) load_block<BITS>(pw + min(4 * u + 2 * h + s, kb - 1) * BITS, w[s]);
-    };
-
-    f32x16 acc[kMT];
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
-
-    auto products = [&](const uint32_t (&w)[BITS], int t) {
-        const uint8_t* from = xl + (t & 1) * (kTileM * kPitch) + r * kPitch;
-        const int block = (t >> 1) * 4 + 2 * h + (t & 1);
-        const uint32_t g = sbw[min(block >> GSHIFT, gpr - 1)];
-        f16x8 o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = weight_operand<BITS>(w, q, g);
-#pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-            if (i >= turns) break;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const f16x8 v = *reinterpret_cast<const f16x8*>(from + i * 32 * kPitch + ((4 * h + q) ^ (r >> 1 & 7)) * 16);
-                acc[i] = mfma32x32x16<true>(v, o[q], acc[i]);
-            }
-        }
-    };
-
-    const int stages = 2 * units;
-    load_x(0);
-    load_w(wq[0], 0);
-    store_x(0);
-    load_x(1);
-    for (int u = 0; u < units; u += 2) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int t = 2 * u + s;
-            if (t >= stages) break;
-            __syncthreads();  // stage t is there; nobody reads the other place any more
-            if (s % 2 == 0) load_w(wq[(s / 2 + 1) & 1], min(u + s / 2 + 1, units - 1));
-            if (t + 1 < stages) store_x(t + 1);
-            if (t + 2 < stages) load_x(t + 2);
-            products(wq[s / 2][s & 1], t);
-        }
-    }
-
-#pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-        if (i >= turns) break;
-        if constexpr (DOWN) {
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-                if (row < rows && wrow < a.n)
-                    a.d[(int64_t)pair[row] * a.n + wrow] = acc[i][v] * (row_scale[row] * col_scale);
-            }
-        } else {
-            // lanes r < 16 hold gate and r >= 16 up results: exchanged in pairs of rows, lanes with r < 16 keep row v
-            // and the others row v + 1
-            const float other = __shfl_xor(col_scale, 16, 64);
-            const float gs = r < 16 ? col_scale : other, us = r < 16 ? other : col_scale;
-#pragma unroll
-            for (int v = 0; v < 16; v += 2) {
-                uint32_t x0 = __float_as_uint(acc[i][v]), x1 = __float_as_uint(acc[i][v + 1]);
-                swap16(x0, x1);
-                const int vv = v + (r >> 4);
-                const int row = 32 * i + 8 * (vv >> 2) + 4 * h + (vv & 3);
-                const float xs = row_scale[row];
-                const float hv = silu_f32(__uint_as_float(x0) * gs * xs) * (__uint_as_float(x1) * us * xs);
-                // the 16 lanes of a row: their power of two
-                float m = fabsf(hv);
-#pragma unroll
-                for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-                const int ex = min(max((int)(__float_as_uint(m) >> 23), 1), 254) - 127;
-                if (row < rows && 64 * tn + 16 * wave < a.n) {
-                    const int64_t at = row0 + row;
-                    a.h[at * a.n + wrow] = f32_to_half_bits<true>(ldexpf(hv, -ex));
-                    if ((r & 15) == 0) a.h_exp_out[at * (a.n / 16) + (64 * tn + 16 * wave) / 16] = (int8_t)ex;
-                }
-            }
-        }
-    }
+    // as many turns as the rows need: 64, 128, 160 or 192 rows (a tile of an expert with 128 rows on average has
+    // 4 or 5 turns' rows)
+    if (c.rows <= 64) gemm_tile<BITS, DOWN, 2>(a, c, tid);
+    else if (c.rows <= 128) gemm_tile<BITS, DOWN, 4>(a, c, tid);
+    else if (c.rows <= 160) gemm_tile<BITS, DOWN, 5>(a, c, tid);
+    else gemm_tile<BITS, DOWN, 6>(a, c, tid);
 }
 
 // ---- launches -----------------------------------------------------------------------------------------
 
 struct MoeSpace {  // byte offsets into the workspace
-    int64_t xh, x_scale, order, offsets, h, h_exp, d, bytes;
+    int64_t xh, x_scale, order, offsets, h, h_exp, h_most, d, bytes;
 };
 inline MoeSpace moe_gemm_space(int64_t tokens, int64_t width, int64_t hidden, int64_t top_k, int64_t experts) {
     const int64_t pairs = tokens * top_k;
@@ -400,6 +485,7 @@ inline MoeSpace moe_gemm_space(int64_t tokens, int64_t width, int64_t hidden, in
     s.offsets = take((experts + 1) * 4);
     s.h = take(pairs * hidden * 2);
     s.h_exp = take(pairs * (hidden / 16));
+    s.h_most = take(pairs * 4);
     s.d = take(pairs * width * 4);
     s.bytes = at;
     return s;
@@ -411,8 +497,8 @@ inline int64_t gemm_tiles(const MoeArgs& a) {
     return round_up(pairs / kTileM + std::min(pairs, (int64_t)a.experts), 8);
 }
 
-template <int BITS, int GSHIFT, bool F16>
-hipError_t launch_gemm_path(const MoeArgs& a, hipStream_t stream) {
+template <int BITS>
+hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     const int64_t pairs = a.tokens * a.top_k;
     const MoeSpace s = moe_gemm_space(a.tokens, a.width, a.hidden, a.top_k, a.experts);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -420,44 +506,46 @@ hipError_t launch_gemm_path(const MoeArgs& a, hipStream_t stream) {
     float* x_scale = reinterpret_cast<float*>(ws + s.x_scale);
     int32_t* order = reinterpret_cast<int32_t*>(ws + s.order);
     int32_t* offsets = reinterpret_cast<int32_t*>(ws + s.offsets);
-    const int64_t convert = F16 ? 0 : (a.tokens + kSortThreads / 64 - 1) / (kSortThreads / 64);
+    GemmArgs g{};
+    g.h_most = reinterpret_cast<int32_t*>(ws + s.h_most);
+    const int64_t convert = f16 ? 0 : (a.tokens + kSortThreads / 64 - 1) / (kSortThreads / 64);
     moe_sort_kernel<<<dim3((unsigned)(a.experts + convert)), dim3(kSortThreads), 0, stream>>>(
-        a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens, a.width, xh, x_scale);
+        a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens, a.width, xh, x_scale, g.h_most);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    GemmArgs g{};
     g.order = order;
     g.offsets = offsets;
     g.weights = a.weights;
     g.top_k = a.top_k;
     g.experts = a.experts;
+    g.gshift = a.group == 32 ? 0 : a.group == 64 ? 1 : 2;
+    g.f16 = f16;
     const int64_t tiles = gemm_tiles(a);
-    g.x = F16 ? a.x : xh;
-    g.x_scale = F16 ? nullptr : x_scale;
+    g.x = f16 ? a.x : xh;
+    g.x_scale = f16 ? nullptr : x_scale;
     g.w0 = a.gate;
     g.w1 = a.up;
     g.h = reinterpret_cast<uint16_t*>(ws + s.h);
-    g.h_exp_out = reinterpret_cast<int8_t*>(ws + s.h_exp);
+    g.h_exp = reinterpret_cast<int8_t*>(ws + s.h_exp);
     g.k = a.width;
     g.n = a.hidden;
     g.tiles_n = (a.hidden + 63) / 64;
-    moe_gemm_kernel<BITS, GSHIFT, F16, false><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
-                                               gemm_lds_bytes(a.width, a.group), stream>>>(g);
+    moe_gemm_kernel<BITS, false><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
+                                   gemm_lds_bytes(a.width, a.group), stream>>>(g);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.x = g.h;
     g.x_scale = nullptr;
-    g.h_exp = g.h_exp_out;
     g.w0 = g.w1 = a.down;
     g.d = reinterpret_cast<float*>(ws + s.d);
     g.k = a.hidden;
     g.n = a.width;
     g.tiles_n = (a.width + 127) / 128;
-    moe_gemm_kernel<BITS, GSHIFT, F16, true><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
-                                              gemm_lds_bytes(a.hidden, a.group), stream>>>(g);
+    moe_gemm_kernel<BITS, true><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
+                                  gemm_lds_bytes(a.hidden, a.group), stream>>>(g);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    return launch_combine<F16>(a, g.d, stream);
+    return f16 ? launch_combine<true>(a, g.d, stream) : launch_combine<false>(a, g.d, stream);
 }
 
 // Whether the GEMM serves a call: from an average of 24 rows an expert on, where the scales of 128 weight rows fit
@@ -466,29 +554,6 @@ inline bool gemm_path(const MoeArgs& a) {
     const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1;
     return a.tokens * a.top_k >= (int64_t)24 * a.experts && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
            gemm_lds_bytes(a.hidden, a.group) <= kGemmMaxLds;
-}
-
-template <int BITS, bool F16>
-hipError_t launch_moe_bits(const MoeArgs& a, hipStream_t stream) {
-    if (!gemm_path(a)) return launch_few_bits<BITS, F16>(a, stream);
-    if (a.group == 32) return launch_gemm_path<BITS, 0, F16>(a, stream);
-    if (a.group == 64) return launch_gemm_path<BITS, 1, F16>(a, stream);
-    return launch_gemm_path<BITS, 2, F16>(a, stream);
-}
-
-template <bool F16>
-hipError_t launch_moe(const MoeArgs& a, hipStream_t stream) {
-    if (a.top_k == 0 || a.experts == 0 || a.hidden == 0) return launch_combine<F16>(a, nullptr, stream);
-    switch (a.bits) {
-        case 1: return launch_moe_bits<1, F16>(a, stream);
-        case 2: return launch_moe_bits<2, F16>(a, stream);
-        case 3: return launch_moe_bits<3, F16>(a, stream);
-        case 4: return launch_moe_bits<4, F16>(a, stream);
-        case 5: return launch_moe_bits<5, F16>(a, stream);
-        case 6: return launch_moe_bits<6, F16>(a, stream);
-        case 8: return launch_moe_bits<8, F16>(a, stream);
-        default: return hipErrorInvalidValue;
-    }
 }
 
 }  // namespace
