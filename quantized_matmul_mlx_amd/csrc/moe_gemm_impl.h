@@ -3,8 +3,8 @@
 //
 //   1. moe_sort: the pairs of each expert in their order (a workgroup an expert looks through all pairs), and x
 //      as float16 rows;
-//   2. gate and up: h = silu(g) u of up to 192 rows x 64 columns a workgroup;
-//   3. down: d of up to 192 rows x 128 columns;
+//   2. gate and up: h = silu(g) u of up to 160 rows x 64 columns a workgroup;
+//   3. down: d of up to 160 rows x 128 columns;
 //   4. moe_combine (moe_few_impl.h).
 //
 // Weights become float16 operands, rounded once to 11 bits, by two instructions for two codes: a code alone
@@ -28,11 +28,12 @@
 namespace qaff {
 namespace {
 
-constexpr int kMT = 6;                 // turns of 32 rows a workgroup takes at most
-constexpr int kTileM = 32 * kMT;       // rows
+constexpr int kTileM = 160;            // rows a workgroup takes at most, in turns of 32
 constexpr int kGemmThreads = 256;
 constexpr int kStep = 64;              // codes a stage of x
 constexpr int kPitch = 2 * kStep;      // bytes of a row of a stage
+constexpr int kStages = 3;
+constexpr int kStageBytes = kTileM * kPitch;
 
 struct GemmArgs {
     const uint16_t* x;       // float16 rows of k values: [tokens] (DOWN false) or [sorted pairs]
@@ -161,36 +162,34 @@ __device__ __forceinline__ uint32_t fma2(uint32_t c, h2 s, h2 b) {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(h2, c), s, b));
 }
 
-// Octet j of a block: codes times s + b. sb: the group's s 2^24 and b (float16 bits, low and high half).
-// 4-bit codes come in the order c0 c4 c1 c5 c2 c6 c3 c7 (x is staged in it).
-template <int BITS>
-__device__ __forceinline__ f16x8 weight_operand(const uint32_t (&w)[BITS], int j, uint32_t sb) {
+// A group's scale and bias, both halves each: s 2^24, that / 16 (for 4-bit codes that stay in bits 4 .. 7) and b.
+struct GroupOf {
+    h2 s, s16, b;
+};
+__device__ __forceinline__ GroupOf group_of(uint32_t sb) {
     const uint32_t lo = sb & 0xffffu, hi = sb >> 16;
-    const h2 s = __builtin_bit_cast(h2, lo | lo << 16), b = __builtin_bit_cast(h2, hi | hi << 16);
-    u32x4a o;
+    const h2 s = __builtin_bit_cast(h2, lo | lo << 16);
+    return GroupOf{s, s * (h2){(_Float16)0.0625f, (_Float16)0.0625f}, __builtin_bit_cast(h2, hi | hi << 16)};
+}
+
+// Word e of octet j of a block: two codes times s + b. 4-bit codes come in the order c0 c4 c1 c5 c2 c6 c3 c7 (x is
+// staged in it).
+template <int BITS>
+__device__ __forceinline__ uint32_t weight_word(const uint32_t (&w)[BITS], int j, int e, const GroupOf& g) {
     if constexpr (BITS == 4) {
-        const h2 s16 = s * (h2){(_Float16)0.0625f, (_Float16)0.0625f};
-        const uint32_t v = w[j], v8 = v >> 8;
-        o[0] = fma2(v & 0x000F000Fu, s, b);
-        o[1] = fma2(v & 0x00F000F0u, s16, b);
-        o[2] = fma2(v8 & 0x000F000Fu, s, b);
-        o[3] = fma2(v8 & 0x00F000F0u, s16, b);
+        const uint32_t v = e & 2 ? w[j] >> 8 : w[j];
+        return e & 1 ? fma2(v & 0x00F000F0u, g.s16, g.b) : fma2(v & 0x000F000Fu, g.s, g.b);
     } else if constexpr (BITS == 8) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = fma2(__builtin_amdgcn_perm(0u, w[2 * j + (q >> 1)], q & 1 ? 0x0c030c02u : 0x0c010c00u), s, b);
+        return fma2(__builtin_amdgcn_perm(0u, w[2 * j + (e >> 1)], e & 1 ? 0x0c030c02u : 0x0c010c00u), g.s, g.b);
     } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            o[q] = fma2(code_at<BITS>(w, 8 * j + 2 * q) | code_at<BITS>(w, 8 * j + 2 * q + 1) << 16, s, b);
+        return fma2(code_at<BITS>(w, 8 * j + 2 * e) | code_at<BITS>(w, 8 * j + 2 * e + 1) << 16, g.s, g.b);
     }
-    return __builtin_bit_cast(f16x8, o);
 }
 
 // ---- the GEMM -----------------------------------------------------------------------------------------
 
-// LDS: two stages of x, then the scales and biases of the 128 weight rows.
-inline int gemm_lds_bytes(int k, int group) { return 2 * kTileM * kPitch + 128 * (k / group + 1) * 4; }
+// LDS: three stages of x, then the scales and biases of the 128 weight rows.
+inline int gemm_lds_bytes(int k, int group) { return kStages * kStageBytes + 128 * (k / group + 1) * 4; }
 constexpr int kGemmMaxLds = 158 * 1024;
 
 // The largest magnitude of the 16 lanes of a row.
@@ -241,32 +240,26 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
         u32x4h x[T];
         int e[T];
     };
-    auto load_x = [&](Ahead& s, int t) {  // columns past the row's end repeat the last ones
+    auto load_x = [&](Ahead& s, int t, int i) {  // columns past the row's end repeat the last ones
         const int col = min((t >> 1) * 128 + (t & 1) * 32 + col_in, a.k - 8);
-#pragma unroll
-        for (int i = 0; i < T; ++i) {
-            s.x[i] = *reinterpret_cast<const u32x4h*>(xp[i] + col);
-            if constexpr (DOWN) s.e[i] = ep[i][col / 16];
-        }
+        s.x[i] = *reinterpret_cast<const u32x4h*>(xp[i] + col);
+        if constexpr (DOWN) s.e[i] = ep[i][col / 16];
     };
-    auto store_x = [&](const Ahead& s, int t) {
+    auto store_x = [&](const Ahead& s, int t, int stage, int i) {
+        u32x4a v = u32x4a{s.x[i].x, s.x[i].y, s.x[i].z, s.x[i].w};
+        if constexpr (DOWN) {  // to the power of two of the row: 2^(e - most), at least 2^-40 (0 in float16)
+            const _Float16 f = (_Float16)__int_as_float((max(s.e[i] - most[i], -40) + 127) << 23);
+            const h2 f2 = {f, f};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (uint32_t)v[q]) * f2);
+        }
+        if constexpr (BITS == 4)
+            v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                       __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
         const bool there = (t >> 1) * 128 + (t & 1) * 32 + col_in < a.k;
 #pragma unroll
-        for (int i = 0; i < T; ++i) {
-            u32x4a v = u32x4a{s.x[i].x, s.x[i].y, s.x[i].z, s.x[i].w};
-            if constexpr (DOWN) {  // to the power of two of the row: 2^(e - most), at least 2^-40 (0 in float16)
-                const _Float16 f = (_Float16)__int_as_float((max(s.e[i] - most[i], -40) + 127) << 23);
-                const h2 f2 = {f, f};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (uint32_t)v[q]) * f2);
-            }
-            if constexpr (BITS == 4)
-                v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                           __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = there ? v[q] : 0u;
-            *reinterpret_cast<u32x4a*>(to[i] + (t & 1) * (kTileM * kPitch)) = v;
-        }
+        for (int q = 0; q < 4; ++q) v[q] = there ? v[q] : 0u;
+        *reinterpret_cast<u32x4a*>(to[i] + stage * kStageBytes) = v;
     };
     // A unit of 128 codes: this lane's blocks 2 h and 2 h + 1 of its four.
     const int units = (a.k + 127) / 128;
@@ -274,61 +267,96 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
 #pragma unroll
         for (int s = 0; s < 2; ++s) load_block<BITS>(c.pw + min(4 * min(u, units - 1) + 2 * h + s, kb - 1) * BITS, w[s]);
     };
+    auto group_at = [&](int t) {
+        return group_of(c.sb[min(((t >> 1) * 4 + 2 * h + (t & 1)) >> a.gshift, gpr - 1)]);
+    };
     f32x16 acc[T];
 #pragma unroll
     for (int i = 0; i < T; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][v] = 0.f;
-    auto products = [&](const uint32_t (&w)[BITS], int t) {
-        const uint8_t* from = c.xl + (t & 1) * (kTileM * kPitch) + r * kPitch;
-        const uint32_t g = c.sb[min(((t >> 1) * 4 + 2 * h + (t & 1)) >> a.gshift, gpr - 1)];
-        uint32_t own[BITS];
+
+    // The products of a stage are 4 T, n = q T + i for octet q and turn i. The x operand of each is read kDepth products
+    // ahead (a read takes longer than a product), over the border of two stages too, and the weight operand of the next
+    // octet is formed word by word beside them; so are the stores and loads of x.
+    constexpr int kDepth = T == 5 ? 5 : 8, kCount = 4 * T;
+    static_assert(kCount % kDepth == 0, "the operands' places turn with the stages");
+    f16x8 f[kDepth];
+    auto read = [&](int stage, int n) {
+        return *reinterpret_cast<const f16x8*>(c.xl + stage * kStageBytes + (n % T * 32 + r) * kPitch +
+                                               ((4 * h + n / T) ^ (r >> 1 & 7)) * 16);
+    };
+    u32x4a o;  // the weight operand of the next octet
+    auto step = [&](int t, int stage, const uint32_t (&w)[BITS], const uint32_t (&follow)[BITS], GroupOf& g, Ahead& x) {
+        uint32_t own[BITS], next[BITS];
 #pragma unroll
         for (int i = 0; i < BITS; ++i) {
             own[i] = w[i];
-            asm volatile("" : "+v"(own[i]));  // here, not where the loads are issued, which would wait for them
+            next[i] = follow[i];
+            // here, not where the loads are issued, which would wait for them
+            asm volatile("" : "+v"(own[i]), "+v"(next[i]));
         }
+        const GroupOf gn = group_at(t + 1);
+        // After this barrier nobody reads stage t - 1 any more, whose place stage t + 2 takes; stage t + 1, stored one
+        // step ago, is there.
+        __syncthreads();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const f16x8 o = weight_operand<BITS>(own, q, g);
+            const f16x8 now = __builtin_bit_cast(f16x8, o);
 #pragma unroll
-            for (int i = 0; i < T; ++i)
-                acc[i] = mfma32x32x16<true>(
-                    *reinterpret_cast<const f16x8*>(from + i * 32 * kPitch + ((4 * h + q) ^ (r >> 1 & 7)) * 16), o, acc[i]);
+            for (int i = 0; i < T; ++i) {
+                const int n = q * T + i;
+                acc[i] = mfma32x32x16<true>(f[n % kDepth], now, acc[i]);
+                f[n % kDepth] = n + kDepth < kCount ? read(stage, n + kDepth) : read((stage + 1) % kStages, n + kDepth - kCount);
+                if (n < T) store_x(x, t + 2, (stage + 2) % kStages, n);
+                else if (n < 2 * T) load_x(x, t + 4, n - T);
+#pragma unroll
+                for (int e = 4 * i / T; e < 4 * (i + 1) / T; ++e)
+                    o[e] = q < 3 ? weight_word<BITS>(own, q + 1, e, g) : weight_word<BITS>(next, 0, e, gn);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
+        g = gn;
     };
 
-    // x: a stage in LDS while one is multiplied, two more in registers. Weights: a unit and two more.
-    const int stages = 2 * units;
     Ahead xa, xb;
     uint32_t w0[2][BITS], w1[2][BITS], w2[2][BITS];
-    load_x(xa, 0);
+#pragma unroll
+    for (int i = 0; i < T; ++i) load_x(xa, 0, i);
     load_w(w0, 0);
-    load_x(xb, 1);
+#pragma unroll
+    for (int i = 0; i < T; ++i) load_x(xb, 1, i);
     load_w(w1, 1);
-    store_x(xa, 0);
-    load_x(xa, 2);
-    auto unit = [&](int u, const uint32_t (&w)[2][BITS], uint32_t (&next)[2][BITS]) {
-        const int t = 2 * u;
-        __syncthreads();  // stage t is there; nobody reads the other place any more
-        store_x(xb, t + 1);
-        load_x(xb, t + 3);
-        load_w(next, u + 2);
-        products(w[0], t);
-        __syncthreads();
-        store_x(xa, t + 2);
-        load_x(xa, t + 4);
-        products(w[1], t + 1);
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        store_x(xa, 0, 0, i);
+        load_x(xa, 2, i);
+    }
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        store_x(xb, 1, 1, i);
+        load_x(xb, 3, i);
+    }
+    GroupOf g = group_at(0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = weight_word<BITS>(w0[0], 0, e, g);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kDepth; ++n) f[n] = read(0, n);
+    auto unit = [&](int u, int stage, const uint32_t (&w)[2][BITS], const uint32_t (&follow)[2][BITS],
+                    uint32_t (&free)[2][BITS]) {
+        load_w(free, u + 2);
+        step(2 * u, stage, w[0], w[1], g, xa);
+        step(2 * u + 1, (stage + 1) % kStages, w[1], follow[0], g, xb);
     };
-    for (int u = 0;; u += 3) {
-        unit(u, w0, w2);
+    for (int u = 0;; u += 3) {  // six steps: the stages and the weights' registers turn
+        unit(u, 0, w0, w1, w2);
         if (u + 1 >= units) break;
-        unit(u + 1, w1, w0);
+        unit(u + 1, 2, w1, w2, w0);
         if (u + 2 >= units) break;
-        unit(u + 2, w2, w1);
+        unit(u + 2, 1, w2, w0, w1);
         if (u + 3 >= units) break;
     }
-    (void)stages;
 
 #pragma unroll
     for (int i = 0; i < T; ++i) {
@@ -447,7 +475,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     for (int g = h; g < gpr; g += 2) top = fmaxf(top, fmaxf(fabsf(value(sp[g])), fabsf(value(bp[g])) * 0x1p-20f));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int up = min(14 + 127 - max(min((int)(__float_as_uint(top) >> 23), 254), 1), 120);
-    c.sb = reinterpret_cast<uint32_t*>(smem + 2 * kTileM * kPitch) + (32 * wave + r) * spitch;
+    c.sb = reinterpret_cast<uint32_t*>(smem + kStages * kStageBytes) + (32 * wave + r) * spitch;
 #pragma unroll 8
     for (int g = h; g < gpr; g += 2) c.sb[g] = pack_half2<true>(ldexpf(value(sp[g]), up), ldexpf(value(bp[g]), up - 24));
     c.col_scale = ldexpf(1.f, 24 - up);
@@ -457,12 +485,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     c.most = most;
     c.row_scale = row_scale;
     __syncthreads();
-    // as many turns as the rows need: 64, 128, 160 or 192 rows (a tile of an expert with 128 rows on average has
-    // 4 or 5 turns' rows)
+    // as many turns as the rows need: 64, 128 or 160 rows (of an expert with 128 rows on average nearly all fit)
     if (c.rows <= 64) gemm_tile<BITS, DOWN, 2>(a, c, tid);
     else if (c.rows <= 128) gemm_tile<BITS, DOWN, 4>(a, c, tid);
-    else if (c.rows <= 160) gemm_tile<BITS, DOWN, 5>(a, c, tid);
-    else gemm_tile<BITS, DOWN, 6>(a, c, tid);
+    else gemm_tile<BITS, DOWN, 5>(a, c, tid);
 }
 
 // ---- launches -----------------------------------------------------------------------------------------
