@@ -36,20 +36,25 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = kTileM * kPitch;
 
 struct GemmArgs {
-    const uint16_t* x;       // float16 rows of k values: [tokens] (DOWN false) or [sorted pairs]
-    const float* x_scale;    // [tokens] what a row of x was divided by, or null
+    const uint16_t* x;       // float16 rows of pad(k) values: [tokens] (DOWN false) or [sorted pairs]
+    const float* x_scale;    // [tokens] what a row of x was divided by
     int8_t* h_exp;           // [sorted pairs, hidden / 16] exponents of h
     int32_t* h_most;         // [sorted pairs] the largest of them, + 128
     ExpertWeight w0, w1;
     const int32_t* order;    // [pairs]: sorted position -> pair
     const int32_t* offsets;  // [experts + 1]
     const float* weights;    // [pairs]
-    uint16_t* h;             // [sorted pairs, n]
+    uint16_t* h;             // [sorted pairs, pad(n)]
     float* d;                // [pairs, n]
     int k, n, top_k, experts, tiles_n;
     int gshift;              // group size 32 << gshift
     int f16;                 // type of scales and biases
 };
+
+// Rows of x and h end with zeros up to a whole unit of 128 values. With 4-bit codes each 8 values lie in the order of
+// their operands, 0 4 1 5 2 6 3 7.
+__host__ __device__ constexpr int pad_unit(int k) { return (k + 127) / 128 * 128; }
+__host__ __device__ constexpr int operand_place(int i) { return (i & ~7) | (i & 3) << 1 | (i >> 2 & 1); }
 
 // ---- the order of the pairs, and x as float16 -----------------------------------------------------
 
@@ -74,34 +79,41 @@ __device__ __forceinline__ int sort_less(const int32_t* chosen, int64_t pairs, i
 }
 
 // Workgroup e < experts: offsets[e] = pairs of lower experts, order[offsets[e] ..] = its pairs. The others: rows
-// of x, a wave each, divided by a power of two that puts the largest value into [2^14, 2^15).
+// of x in float16, a wave each, divided by a power of two that puts the largest value into [2^14, 2^15).
+template <bool F16>
 __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* chosen, int64_t pairs, int experts,
                                                                 int32_t* order, int32_t* offsets, const uint16_t* x,
-                                                                int64_t tokens, int width, uint16_t* xh, float* x_scale,
-                                                                int32_t* h_most) {
+                                                                int64_t tokens, int width, uint16_t* xh, float* x_scale, int fours,
+                                                                int hidden, uint16_t* h, int32_t* h_most) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int pitch = pad_unit(width);
     if ((int)blockIdx.x >= experts) {
         const int64_t t = (int64_t)(blockIdx.x - experts) * (kSortThreads / 64) + wave;
         if (t >= tokens) return;
         const uint16_t* src = x + t * width;
+        auto value = [&](uint32_t v) { return F16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
         float top = 0.f;
         for (int c = lane * 8; c < width; c += 512) {
             const u32x4h v = *reinterpret_cast<const u32x4h*>(src + c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                top = fmaxf(top, fmaxf(fabsf(bf16_to_f32(v[q])), fabsf(__uint_as_float(v[q] & 0xffff0000u))));
+            for (int q = 0; q < 4; ++q) top = fmaxf(top, fmaxf(fabsf(value(v[q])), fabsf(value(v[q] >> 16))));
         }
 #pragma unroll
         for (int s = 32; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
         const int ex = min((int)(__float_as_uint(top) >> 23), 254);     // infinities stay so
         const int up = min(14 + 127 - max(ex, 1), 120);                 // 2^up takes the largest to [2^14, 2^15)
-        for (int c = lane * 8; c < width; c += 512) {
-            const u32x4h v = *reinterpret_cast<const u32x4h*>(src + c);
-            u32x4a o;
+        for (int c = lane * 8; c < pitch; c += 512) {
+            u32x4a o = u32x4a{0u, 0u, 0u, 0u};
+            if (c < width) {
+                const u32x4h v = *reinterpret_cast<const u32x4h*>(src + c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                o[q] = pack_half2<true>(ldexpf(bf16_to_f32(v[q]), up), ldexpf(__uint_as_float(v[q] & 0xffff0000u), up));
-            *reinterpret_cast<u32x4a*>(xh + t * width + c) = o;
+                for (int q = 0; q < 4; ++q)
+                    o[q] = pack_half2<true>(ldexpf(value(v[q]), up), ldexpf(value(v[q] >> 16), up));
+                if (fours)
+                    o = u32x4a{__builtin_amdgcn_perm(o.z, o.x, 0x05040100u), __builtin_amdgcn_perm(o.z, o.x, 0x07060302u),
+                               __builtin_amdgcn_perm(o.w, o.y, 0x05040100u), __builtin_amdgcn_perm(o.w, o.y, 0x07060302u)};
+            }
+            *reinterpret_cast<u32x4a*>(xh + t * pitch + c) = o;
         }
         if (lane == 0) x_scale[t] = ldexpf(1.f, -up);
         return;
@@ -148,6 +160,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* c
         __syncthreads();
     }
     for (int i = tid; i < total; i += kSortThreads) h_most[base + i] = 0;
+    const int zeros = pad_unit(hidden) - hidden;  // of each of its rows of h
+    for (int i = tid; i < total * zeros; i += kSortThreads)
+        h[(int64_t)(base + i / zeros) * pad_unit(hidden) + hidden + i % zeros] = 0;
     if (tid == 0) {
         offsets[e] = base;
         if (e == experts - 1) offsets[experts] = base + total;
@@ -205,6 +220,8 @@ struct GemmTile {
     const uint32_t* pw;      // this lane's weight row
     uint32_t* sb;            // its scales and biases in LDS
     uint8_t* xl;
+    const uint16_t* x;       // a.x, DOWN: from the tile's first row on
+    const int8_t* exps;      // DOWN: the exponents, from the tile's first row on
     const int *src, *pair;   // [kTileM] in LDS
     const float* row_scale;
     const int* most;         // DOWN: h_most of the row, + 128
@@ -222,47 +239,42 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
     // This thread's pieces of a stage: row i * 32 + tid / 8, 16 bytes at slot tid % 8. Stage t = 2 u + s holds codes
     // 128 u + 32 s .. + 31 (k-slot 0) and 128 u + 64 + 32 s .. (k-slot 1).
     const int piece = tid & 7, col_in = (piece >> 2) * 64 + (piece & 3) * 8;
-    const uint16_t* xp[T];
-    const int8_t* ep[T];
+    const int pitch = pad_unit(a.k);
+    uint32_t xp[T], ep[T];  // bytes from c.x and c.exps on
     int most[T];
     uint8_t* to[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         const int row = i * 32 + tid / 8;
-        xp[i] = a.x + (int64_t)c.src[row] * a.k;
+        xp[i] = (uint32_t)(c.src[row] * pitch + col_in) * 2u;
         if constexpr (DOWN) {
-            ep[i] = a.h_exp + (int64_t)c.src[row] * (a.k / 16);
+            ep[i] = (uint32_t)(c.src[row] * (a.k / 16));
             most[i] = c.most[row] - 128;
         }
         to[i] = c.xl + row * kPitch + ((piece ^ (row >> 1)) & 7) * 16;
     }
     struct Ahead {
-        u32x4h x[T];
+        u32x4a x[T];
         int e[T];
     };
-    auto load_x = [&](Ahead& s, int t, int i) {  // columns past the row's end repeat the last ones
-        const int col = min((t >> 1) * 128 + (t & 1) * 32 + col_in, a.k - 8);
-        s.x[i] = *reinterpret_cast<const u32x4h*>(xp[i] + col);
-        if constexpr (DOWN) s.e[i] = ep[i][col / 16];
+    const int units = pitch / 128;
+    auto load_x = [&](Ahead& s, int t, int i) {  // stages past the last one repeat it
+        t = min(t, 2 * units - 1);
+        const int col = (t >> 1) * 128 + (t & 1) * 32;
+        s.x[i] = *reinterpret_cast<const u32x4a*>(reinterpret_cast<const uint8_t*>(c.x + col) + xp[i]);
+        if constexpr (DOWN) s.e[i] = c.exps[ep[i] + (uint32_t)min((col + col_in) / 16, a.k / 16 - 1)];
     };
-    auto store_x = [&](const Ahead& s, int t, int stage, int i) {
-        u32x4a v = u32x4a{s.x[i].x, s.x[i].y, s.x[i].z, s.x[i].w};
+    auto store_x = [&](const Ahead& s, int stage, int i) {
+        u32x4a v = s.x[i];
         if constexpr (DOWN) {  // to the power of two of the row: 2^(e - most), at least 2^-40 (0 in float16)
             const _Float16 f = (_Float16)__int_as_float((max(s.e[i] - most[i], -40) + 127) << 23);
             const h2 f2 = {f, f};
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (uint32_t)v[q]) * f2);
         }
-        if constexpr (BITS == 4)
-            v = u32x4a{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                       __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
-        const bool there = (t >> 1) * 128 + (t & 1) * 32 + col_in < a.k;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = there ? v[q] : 0u;
         *reinterpret_cast<u32x4a*>(to[i] + stage * kStageBytes) = v;
     };
     // A unit of 128 codes: this lane's blocks 2 h and 2 h + 1 of its four.
-    const int units = (a.k + 127) / 128;
     auto load_w = [&](uint32_t (&w)[2][BITS], int u) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) load_block<BITS>(c.pw + min(4 * min(u, units - 1) + 2 * h + s, kb - 1) * BITS, w[s]);
@@ -308,7 +320,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
                 const int n = q * T + i;
                 acc[i] = mfma32x32x16<true>(f[n % kDepth], now, acc[i]);
                 f[n % kDepth] = n + kDepth < kCount ? read(stage, n + kDepth) : read((stage + 1) % kStages, n + kDepth - kCount);
-                if (n < T) store_x(x, t + 2, (stage + 2) % kStages, n);
+                if (n < T) store_x(x, (stage + 2) % kStages, n);
                 else if (n < 2 * T) load_x(x, t + 4, n - T);
 #pragma unroll
                 for (int e = 4 * i / T; e < 4 * (i + 1) / T; ++e)
@@ -329,12 +341,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
     load_w(w1, 1);
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-        store_x(xa, 0, 0, i);
+        store_x(xa, 0, i);
         load_x(xa, 2, i);
     }
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-        store_x(xb, 1, 1, i);
+        store_x(xb, 1, i);
         load_x(xb, 3, i);
     }
     GroupOf g = group_at(0);
@@ -384,7 +396,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
                 const int ex = min(max((int)(__float_as_uint(row_max(fabsf(hv))) >> 23), 1), 254) - 127;
                 if (row < c.rows && 64 * c.tn + 16 * wave < a.n) {
                     const int64_t at = c.row0 + row;
-                    a.h[at * a.n + c.wrow] = f32_to_half_bits<true>(ldexpf(hv, -ex));
+                    a.h[at * pad_unit(a.n) + (BITS == 4 ? operand_place(c.wrow) : c.wrow)] =
+                        f32_to_half_bits<true>(ldexpf(hv, -ex));
                     if ((r & 15) == 0) {
                         a.h_exp[at * (a.n / 16) + (64 * c.tn + 16 * wave) / 16] = (int8_t)ex;
                         atomicMax(a.h_most + at, ex + 128);  // the order does not matter
@@ -450,13 +463,13 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
         const int p = a.order[at];
         if constexpr (DOWN) {
             const int m = a.h_most[at];
-            src[i] = at;
+            src[i] = at - c.row0;
             pair[i] = p;
             most[i] = m;
             row_scale[i] = a.weights[p] * ldexpf(1.f, m - 128);
         } else {
             src[i] = p / a.top_k;
-            row_scale[i] = a.x_scale ? a.x_scale[p / a.top_k] : 1.f;
+            row_scale[i] = a.x_scale[p / a.top_k];
         }
     }
 
@@ -480,6 +493,8 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     for (int g = h; g < gpr; g += 2) c.sb[g] = pack_half2<true>(ldexpf(value(sp[g]), up), ldexpf(value(bp[g]), up - 24));
     c.col_scale = ldexpf(1.f, 24 - up);
     c.xl = smem;
+    c.x = DOWN ? a.x + (int64_t)c.row0 * pad_unit(a.k) : a.x;
+    c.exps = a.h_exp + (DOWN ? (int64_t)c.row0 * (a.k / 16) : 0);
     c.src = src;
     c.pair = pair;
     c.most = most;
@@ -505,11 +520,11 @@ inline MoeSpace moe_gemm_space(int64_t tokens, int64_t width, int64_t hidden, in
         at = round_up(at + bytes, 256);
         return was;
     };
-    s.xh = take(tokens * width * 2);
+    s.xh = take(tokens * pad_unit((int)width) * 2);
     s.x_scale = take(tokens * 4);
     s.order = take(pairs * 4);
     s.offsets = take((experts + 1) * 4);
-    s.h = take(pairs * hidden * 2);
+    s.h = take(pairs * pad_unit((int)hidden) * 2);
     s.h_exp = take(pairs * (hidden / 16));
     s.h_most = take(pairs * 4);
     s.d = take(pairs * width * 4);
@@ -534,9 +549,14 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     int32_t* offsets = reinterpret_cast<int32_t*>(ws + s.offsets);
     GemmArgs g{};
     g.h_most = reinterpret_cast<int32_t*>(ws + s.h_most);
-    const int64_t convert = f16 ? 0 : (a.tokens + kSortThreads / 64 - 1) / (kSortThreads / 64);
-    moe_sort_kernel<<<dim3((unsigned)(a.experts + convert)), dim3(kSortThreads), 0, stream>>>(
-        a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens, a.width, xh, x_scale, g.h_most);
+    g.h = reinterpret_cast<uint16_t*>(ws + s.h);
+    const dim3 sort((unsigned)(a.experts + (a.tokens + kSortThreads / 64 - 1) / (kSortThreads / 64)));
+    if (f16)
+        moe_sort_kernel<true><<<sort, dim3(kSortThreads), 0, stream>>>(a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens,
+                                                                       a.width, xh, x_scale, BITS == 4, a.hidden, g.h, g.h_most);
+    else
+        moe_sort_kernel<false><<<sort, dim3(kSortThreads), 0, stream>>>(a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens,
+                                                                        a.width, xh, x_scale, BITS == 4, a.hidden, g.h, g.h_most);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.order = order;
@@ -547,11 +567,10 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     g.gshift = a.group == 32 ? 0 : a.group == 64 ? 1 : 2;
     g.f16 = f16;
     const int64_t tiles = gemm_tiles(a);
-    g.x = f16 ? a.x : xh;
-    g.x_scale = f16 ? nullptr : x_scale;
+    g.x = xh;
+    g.x_scale = x_scale;
     g.w0 = a.gate;
     g.w1 = a.up;
-    g.h = reinterpret_cast<uint16_t*>(ws + s.h);
     g.h_exp = reinterpret_cast<int8_t*>(ws + s.h_exp);
     g.k = a.width;
     g.n = a.hidden;
@@ -561,7 +580,6 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.x = g.h;
-    g.x_scale = nullptr;
     g.w0 = g.w1 = a.down;
     g.d = reinterpret_cast<float*>(ws + s.d);
     g.k = a.hidden;
@@ -575,10 +593,10 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
 }
 
 // Whether the GEMM serves a call: from an average of 24 rows an expert on, where the scales of 128 weight rows fit
-// LDS beside x and a launch holds the tiles (2^32 threads).
+// LDS beside x, a launch holds the tiles (2^32 threads) and x is addressed in 32 bits.
 inline bool gemm_path(const MoeArgs& a) {
     const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1;
-    return a.tokens * a.top_k >= (int64_t)24 * a.experts && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
+    return a.tokens * a.top_k >= (int64_t)24 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
            gemm_lds_bytes(a.hidden, a.group) <= kGemmMaxLds;
 }
 
