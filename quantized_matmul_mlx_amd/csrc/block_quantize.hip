@@ -22,6 +22,10 @@ __device__ __forceinline__ float wider(float a, float b) {
     return (b != b || b > a) ? b : a;  // a NaN in a stays: no comparison with it is true
 }
 
+template <int CTRL> __device__ __forceinline__ float from_lane(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
 // Eight values from element i on, of which `n` are there (the others 0).
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int n, float (&v)[8]) {
@@ -53,20 +57,41 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int n, float (&v
     }
 }
 
+// x / scale as float32 rounds it, from r = 1 / scale (rounded): q = v r is off by a step and a half at most, and two
+// corrections q + (v - q scale) r, whose remainder a fused multiply-add forms exactly, first bring it within a step and
+// then to the rounded quotient itself. Five instructions for about ten of the division, which is left to scales whose
+// remainders could leave float32's range.
+struct Scale {
+    float s, r;
+    bool plain;  // the corrections hold
+};
+__device__ __forceinline__ Scale make_scale(float s) {
+    return Scale{s, 1.f / s, s >= 0x1p-90f && s <= 0x1p90f};
+}
+
 // e4m3 of v / scale, four at a time.
-__device__ __forceinline__ uint32_t codes4(const float* v, float scale) {
+__device__ __forceinline__ uint32_t codes4(const float* v, const Scale& c) {
     float q[4];
+    if (c.plain) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float d = v[e] / scale;
-        // a scale far below float32's smallest normal value is off by more than a rounding: no code past 448
-        q[e] = scale == 0.f ? 0.f : d != d ? d : fminf(fmaxf(d, -kTop), kTop);
+        for (int e = 0; e < 4; ++e) {
+            q[e] = v[e] * c.r;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) q[e] = __builtin_fmaf(__builtin_fmaf(-q[e], c.s, v[e]), c.r, q[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float d = v[e] / c.s;
+            // a scale far below float32's smallest normal value is off by more than a rounding: no code past 448
+            q[e] = c.s == 0.f ? 0.f : d != d ? d : fminf(fmaxf(d, -kTop), kTop);
+        }
     }
     int r = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], r, true);
 }
 
-__device__ __forceinline__ void store8(uint8_t* p, int n, const float (&v)[8], float scale) {
+__device__ __forceinline__ void store8(uint8_t* p, int n, const float (&v)[8], const Scale& scale) {
     const uint32_t lo = codes4(v, scale), hi = codes4(v + 4, scale);
     if (n >= 8) {
         *reinterpret_cast<u32x2b*>(p) = u32x2b{lo, hi};
@@ -90,10 +115,12 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(BlockQuantArgs a, in
     float top = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = wider(top, fabsf(v[e]));
-#pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) top = wider(top, __shfl_xor(top, d, 16));
+    top = wider(top, from_lane<0xB1>(top));   // lane ^ 1
+    top = wider(top, from_lane<0x4E>(top));   // lane ^ 2
+    top = wider(top, from_lane<0x141>(top));  // mirrored in 8 lanes
+    top = wider(top, from_lane<0x140>(top));  // and in 16
     const float scale = top / kTop;
-    if (n > 0) store8(a.codes + row * a.cols + col, n, v, scale);
+    if (n > 0) store8(a.codes + row * a.cols + col, n, v, make_scale(scale));
     if (threadIdx.x % 16 == 0) a.scales[b] = scale;
 }
 
@@ -119,10 +146,11 @@ __global__ __launch_bounds__(256) void quantize_tiles_kernel(BlockQuantArgs a, i
     if (threadIdx.x % 64 == 0) most[threadIdx.x / 64] = top;
     __syncthreads();
     const float scale = wider(wider(most[0], most[1]), wider(most[2], most[3])) / kTop;
+    const Scale quotient = make_scale(scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t row = row0 + 16 * i;
-        if (row < a.rows && n > 0) store8(a.codes + row * a.cols + col, n, v[i], scale);
+        if (row < a.rows && n > 0) store8(a.codes + row * a.cols + col, n, v[i], quotient);
     }
     if (threadIdx.x == 0) a.scales[blockIdx.y * kb + blockIdx.x] = scale;
 }

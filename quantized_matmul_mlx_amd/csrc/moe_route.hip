@@ -16,27 +16,51 @@
 namespace qaff {
 namespace {
 
-// Lanes that hold one token's logits: lane i of the group has experts i, i + LANES, ...
-template <int LANES, typename T>
-__device__ __forceinline__ T group_max(T v) {
-#pragma unroll
-    for (int d = LANES / 2; d >= 1; d >>= 1) {
-        const T o = __shfl_xor(v, d, 64);
-        v = o > v ? o : v;
+// Lanes that hold one token's logits: lane i of the group has experts i, i + LANES, ... The exchanges below stay in
+// registers: a read from another lane through LDS takes as long as the rest of a round.
+template <int CTRL, typename T> __device__ __forceinline__ T from_lane(T v) {
+    if constexpr (sizeof(T) == 8) {
+        const int64_t b = __builtin_bit_cast(int64_t, v);
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xf, 0xf, false);
+        return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
     }
+}
+// The value 16 (32) lanes on or before.
+template <bool WIDE> __device__ __forceinline__ uint32_t other_half(uint32_t v) {
+    const bool upper = threadIdx.x & (WIDE ? 32 : 16);
+    const auto r = WIDE ? __builtin_amdgcn_permlane32_swap(v, v, false, false) : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return upper ? r[0] : r[1];
+}
+template <bool WIDE, typename T> __device__ __forceinline__ T from_half(T v) {
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        return __builtin_bit_cast(T, (uint64_t)other_half<WIDE>((uint32_t)(b >> 32)) << 32 | other_half<WIDE>((uint32_t)b));
+    } else {
+        return __builtin_bit_cast(T, other_half<WIDE>(__builtin_bit_cast(uint32_t, v)));
+    }
+}
+template <int LANES, typename T, typename Op>
+__device__ __forceinline__ T group_reduce(T v, Op op) {
+    static_assert(LANES >= 16, "a row of 16 lanes at least");
+    v = op(v, from_lane<0xB1>(v));   // lane ^ 1
+    v = op(v, from_lane<0x4E>(v));   // lane ^ 2
+    v = op(v, from_lane<0x141>(v));  // mirrored in 8 lanes
+    v = op(v, from_lane<0x140>(v));  // and in 16
+    if constexpr (LANES >= 32) v = op(v, from_half<false>(v));
+    if constexpr (LANES >= 64) v = op(v, from_half<true>(v));
     return v;
 }
-template <int LANES>
-__device__ __forceinline__ int group_min(int v) {
-#pragma unroll
-    for (int d = LANES / 2; d >= 1; d >>= 1) v = min(v, __shfl_xor(v, d, 64));
-    return v;
+template <int LANES, typename T> __device__ __forceinline__ T group_max(T v) {
+    return group_reduce<LANES>(v, [](T a, T b) { return b > a ? b : a; });
 }
-template <int LANES, typename T>
-__device__ __forceinline__ T group_sum(T v) {
-#pragma unroll
-    for (int d = LANES / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+template <int LANES> __device__ __forceinline__ int group_min(int v) {
+    return group_reduce<LANES>(v, [](int a, int b) { return min(a, b); });
+}
+template <int LANES, typename T> __device__ __forceinline__ T group_sum(T v) {
+    return group_reduce<LANES>(v, [](T a, T b) { return a + b; });
 }
 
 template <typename K> struct Math;
@@ -118,7 +142,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
             const K most = group_max<LANES>(best);
             const int who = group_min<LANES>(best == most ? at : 1 << 30);
             if (who == at) taken |= 1u << (at / LANES);
-            at_x = __shfl(at_x, who % LANES, LANES);
+            if (a.bias) at_x = __shfl(at_x, who % LANES, LANES);
+            else at_x = most;  // the key is the logit
             if (lane == r) {
                 mine[j] = who;
                 mine_x[j] = at_x;
