@@ -38,8 +38,7 @@ constexpr int kStageBytes = kTileM * kPitch;
 struct GemmArgs {
     const uint16_t* x;       // float16 rows of pad(k) values: [tokens] (DOWN false) or [sorted pairs]
     const float* x_scale;    // [tokens] what a row of x was divided by
-    int8_t* h_exp;           // [sorted pairs, hidden / 16] exponents of h
-    int32_t* h_most;         // [sorted pairs] the largest of them, + 128
+    uint8_t* h_exp;          // [sorted pairs, hidden / 16] exponents of h, + 128
     ExpertWeight w0, w1;
     const int32_t* order;    // [pairs]: sorted position -> pair
     const int32_t* offsets;  // [experts + 1]
@@ -84,7 +83,7 @@ template <bool F16>
 __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* chosen, int64_t pairs, int experts,
                                                                 int32_t* order, int32_t* offsets, const uint16_t* x,
                                                                 int64_t tokens, int width, uint16_t* xh, float* x_scale, int fours,
-                                                                int hidden, uint16_t* h, int32_t* h_most) {
+                                                                int hidden, uint16_t* h) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int pitch = pad_unit(width);
     if ((int)blockIdx.x >= experts) {
@@ -159,7 +158,6 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* c
         total += __shfl(upto, 63, 64);
         __syncthreads();
     }
-    for (int i = tid; i < total; i += kSortThreads) h_most[base + i] = 0;
     const int zeros = pad_unit(hidden) - hidden;  // of each of its rows of h
     for (int i = tid; i < total * zeros; i += kSortThreads)
         h[(int64_t)(base + i / zeros) * pad_unit(hidden) + hidden + i % zeros] = 0;
@@ -215,16 +213,32 @@ __device__ __forceinline__ float row_max(float v) {
     return fmaxf(v, __int_as_float(dpp<0x140, 0xf>(__float_as_int(v))));  // and in 16
 }
 
+// The largest of n bytes.
+__device__ __forceinline__ int most_of(const uint8_t* p, int n) {
+    typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(1)));
+    uint32_t m = 0;
+    int i = 0;
+    for (; i + 16 <= n; i += 16) {
+        const u32x4u v = *reinterpret_cast<const u32x4u*>(p + i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) m = max(m, (uint32_t)v[q] >> (8 * b) & 0xffu);
+    }
+    for (; i < n; ++i) m = max(m, (uint32_t)p[i]);
+    return (int)m;
+}
+
 // What a workgroup finds before its loop.
 struct GemmTile {
     const uint32_t* pw;      // this lane's weight row
     uint32_t* sb;            // its scales and biases in LDS
     uint8_t* xl;
     const uint16_t* x;       // a.x, DOWN: from the tile's first row on
-    const int8_t* exps;      // DOWN: the exponents, from the tile's first row on
+    const uint8_t* exps;     // DOWN: the exponents, from the tile's first row on
     const int *src, *pair;   // [kTileM] in LDS
     const float* row_scale;
-    const int* most;         // DOWN: h_most of the row, + 128
+    const int* most;         // DOWN: the largest exponent of the row, + 128
     float col_scale;
     int row0, rows, wrow, tn;
 };
@@ -249,7 +263,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
         xp[i] = (uint32_t)(c.src[row] * pitch + col_in) * 2u;
         if constexpr (DOWN) {
             ep[i] = (uint32_t)(c.src[row] * (a.k / 16));
-            most[i] = c.most[row] - 128;
+            most[i] = c.most[row];
         }
         to[i] = c.xl + row * kPitch + ((piece ^ (row >> 1)) & 7) * 16;
     }
@@ -399,8 +413,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
                     a.h[at * pad_unit(a.n) + (BITS == 4 ? operand_place(c.wrow) : c.wrow)] =
                         f32_to_half_bits<true>(ldexpf(hv, -ex));
                     if ((r & 15) == 0) {
-                        a.h_exp[at * (a.n / 16) + (64 * c.tn + 16 * wave) / 16] = (int8_t)ex;
-                        atomicMax(a.h_most + at, ex + 128);  // the order does not matter
+                        a.h_exp[at * (a.n / 16) + (64 * c.tn + 16 * wave) / 16] = (uint8_t)(ex + 128);
                     }
                 }
             }
@@ -462,7 +475,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
         const int at = c.row0 + min(i, c.rows - 1);
         const int p = a.order[at];
         if constexpr (DOWN) {
-            const int m = a.h_most[at];
+            const int m = most_of(a.h_exp + (int64_t)at * (a.k / 16), a.k / 16);
             src[i] = at - c.row0;
             pair[i] = p;
             most[i] = m;
@@ -479,18 +492,40 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     const int64_t wr = (int64_t)e * a.n + min(c.wrow, a.n - 1);
     c.pw = W.packed + wr * kb * BITS;
 
-    // scales and biases to LDS, times the power of two of the row: the largest scale 2^24 lies in [2^14, 2^15)
+    // Scales and biases to LDS, times the power of two of the row: the largest scale 2^24 lies in [2^14, 2^15). First as
+    // they are, eight groups a load (the lanes of a row take eights in turn), then changed where they lie.
     const uint16_t* sp = W.scales + wr * gpr;
     const uint16_t* bp = W.biases + wr * gpr;
-    auto value = [&](uint16_t v) { return a.f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
+    c.sb = reinterpret_cast<uint32_t*>(smem + kStages * kStageBytes) + (32 * wave + r) * spitch;
+    for (int g = 8 * h; g < gpr; g += 16) {
+        if (g + 8 <= gpr) {
+            const u32x4h sv = *reinterpret_cast<const u32x4h*>(sp + g), bv = *reinterpret_cast<const u32x4h*>(bp + g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                c.sb[g + 2 * q] = __builtin_amdgcn_perm(bv[q], sv[q], 0x05040100u);
+                c.sb[g + 2 * q + 1] = __builtin_amdgcn_perm(bv[q], sv[q], 0x07060302u);
+            }
+        } else {
+            for (int q = g; q < gpr; ++q) c.sb[q] = (uint32_t)sp[q] | (uint32_t)bp[q] << 16;
+        }
+    }
+    auto value = [&](uint32_t v) { return a.f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
     float top = 0.f;
-#pragma unroll 8
-    for (int g = h; g < gpr; g += 2) top = fmaxf(top, fmaxf(fabsf(value(sp[g])), fabsf(value(bp[g])) * 0x1p-20f));
+    for (int g0 = 8 * h; g0 < gpr; g0 += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t v = c.sb[min(g0 + q, gpr - 1)];
+            top = fmaxf(top, fmaxf(fabsf(value(v)), fabsf(value(v >> 16)) * 0x1p-20f));
+        }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int up = min(14 + 127 - max(min((int)(__float_as_uint(top) >> 23), 254), 1), 120);
-    c.sb = reinterpret_cast<uint32_t*>(smem + kStages * kStageBytes) + (32 * wave + r) * spitch;
-#pragma unroll 8
-    for (int g = h; g < gpr; g += 2) c.sb[g] = pack_half2<true>(ldexpf(value(sp[g]), up), ldexpf(value(bp[g]), up - 24));
+    for (int g0 = 8 * h; g0 < gpr; g0 += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (g0 + q < gpr) {
+                const uint32_t v = c.sb[g0 + q];
+                c.sb[g0 + q] = pack_half2<true>(ldexpf(value(v), up), ldexpf(value(v >> 16), up - 24));
+            }
     c.col_scale = ldexpf(1.f, 24 - up);
     c.xl = smem;
     c.x = DOWN ? a.x + (int64_t)c.row0 * pad_unit(a.k) : a.x;
@@ -509,7 +544,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
 // ---- launches -----------------------------------------------------------------------------------------
 
 struct MoeSpace {  // byte offsets into the workspace
-    int64_t xh, x_scale, order, offsets, h, h_exp, h_most, d, bytes;
+    int64_t xh, x_scale, order, offsets, h, h_exp, d, bytes;
 };
 inline MoeSpace moe_gemm_space(int64_t tokens, int64_t width, int64_t hidden, int64_t top_k, int64_t experts) {
     const int64_t pairs = tokens * top_k;
@@ -526,7 +561,6 @@ inline MoeSpace moe_gemm_space(int64_t tokens, int64_t width, int64_t hidden, in
     s.offsets = take((experts + 1) * 4);
     s.h = take(pairs * pad_unit((int)hidden) * 2);
     s.h_exp = take(pairs * (hidden / 16));
-    s.h_most = take(pairs * 4);
     s.d = take(pairs * width * 4);
     s.bytes = at;
     return s;
@@ -548,15 +582,14 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     int32_t* order = reinterpret_cast<int32_t*>(ws + s.order);
     int32_t* offsets = reinterpret_cast<int32_t*>(ws + s.offsets);
     GemmArgs g{};
-    g.h_most = reinterpret_cast<int32_t*>(ws + s.h_most);
     g.h = reinterpret_cast<uint16_t*>(ws + s.h);
     const dim3 sort((unsigned)(a.experts + (a.tokens + kSortThreads / 64 - 1) / (kSortThreads / 64)));
     if (f16)
         moe_sort_kernel<true><<<sort, dim3(kSortThreads), 0, stream>>>(a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens,
-                                                                       a.width, xh, x_scale, BITS == 4, a.hidden, g.h, g.h_most);
+                                                                       a.width, xh, x_scale, BITS == 4, a.hidden, g.h);
     else
         moe_sort_kernel<false><<<sort, dim3(kSortThreads), 0, stream>>>(a.chosen, pairs, a.experts, order, offsets, a.x, a.tokens,
-                                                                        a.width, xh, x_scale, BITS == 4, a.hidden, g.h, g.h_most);
+                                                                        a.width, xh, x_scale, BITS == 4, a.hidden, g.h);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.order = order;
@@ -571,7 +604,7 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     g.x_scale = x_scale;
     g.w0 = a.gate;
     g.w1 = a.up;
-    g.h_exp = reinterpret_cast<int8_t*>(ws + s.h_exp);
+    g.h_exp = ws + s.h_exp;
     g.k = a.width;
     g.n = a.hidden;
     g.tiles_n = (a.hidden + 63) / 64;
