@@ -658,7 +658,7 @@ hipError_t launch_combine(const MoeArgs& a, const float* d, hipStream_t stream) 
 
 // Whether each pair works alone: the pairs are few beside the experts, and their rows fit LDS.
 inline bool pair_path(const MoeArgs& a) {
-    return a.tokens * a.top_k * 4 <= a.experts && a.hidden <= 4096 && a.top_k <= 64;
+    return a.tokens * a.top_k <= a.experts && a.hidden <= 4096 && a.top_k <= 64;
 }
 
 template <int BITS, int GSHIFT, bool F16>

@@ -159,8 +159,8 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const int32_t* c
         __syncthreads();
     }
     const int zeros = pad_unit(hidden) - hidden;  // of each of its rows of h
-    for (int i = tid; i < total * zeros; i += kSortThreads)
-        h[(int64_t)(base + i / zeros) * pad_unit(hidden) + hidden + i % zeros] = 0;
+    for (int64_t i = tid; i < (int64_t)total * zeros; i += kSortThreads)
+        h[(base + i / zeros) * pad_unit(hidden) + hidden + i % zeros] = 0;
     if (tid == 0) {
         offsets[e] = base;
         if (e == experts - 1) offsets[experts] = base + total;
@@ -438,27 +438,41 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     const int xcd = blockIdx.x % 8, seq = blockIdx.x / 8;
     const int tile = seq / a.tiles_n * 8 + xcd, tn = seq % a.tiles_n;
     if (wave == 0) {  // the expert and the rows of this tile
-        int first = 0, found = -1;
-        for (int base = 0; base < a.experts && found < 0; base += 64) {
-            const int e = min(base + lane, a.experts - 1);
-            const int n = base + lane < a.experts ? a.offsets[e + 1] - a.offsets[e] : 0;
-            const int tiles = (n + kTileM - 1) / kTileM;
+        int first = 0, found = -1, at = 0, end = 0;
+        for (int base = 0; base < a.experts && found < 0; base += 256) {  // four experts a lane
+            int off[5], tiles = 0, mine = 0;
+#pragma unroll
+            for (int j = 0; j < 5; ++j) off[j] = a.offsets[min(base + 4 * lane + j, a.experts)];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tiles += (off[j + 1] - off[j] + kTileM - 1) / kTileM;
             const int upto = first + wave_scan(tiles);
             const uint64_t past = __builtin_amdgcn_ballot_w64(upto > tile);
             if (past) {
                 const int l = __builtin_ctzll(past);
-                found = base + l;
-                first = __shfl(upto - tiles, l, 64);
+                int below = upto - tiles, e = 0, e_first = 0;  // of lane l: which of its experts
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = (off[j + 1] - off[j] + kTileM - 1) / kTileM;
+                    if (tile >= below && tile < below + n) {
+                        e = base + 4 * lane + j;
+                        e_first = below;
+                        at = off[j];
+                        mine = off[j + 1];
+                    }
+                    below += n;
+                }
+                found = __shfl(e, l, 64);
+                first = __shfl(e_first, l, 64);
+                at = __shfl(at, l, 64);
+                end = __shfl(mine, l, 64);
             } else {
                 first = __shfl(upto, 63, 64);
             }
         }
         if (lane == 0) {
             where[0] = found;
-            if (found >= 0) {
-                where[1] = a.offsets[found] + (tile - first) * kTileM;
-                where[2] = a.offsets[found + 1];
-            }
+            where[1] = at + (tile - first) * kTileM;
+            where[2] = end;
         }
     }
     __syncthreads();
@@ -625,11 +639,11 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     return f16 ? launch_combine<true>(a, g.d, stream) : launch_combine<false>(a, g.d, stream);
 }
 
-// Whether the GEMM serves a call: from an average of 24 rows an expert on, where the scales of 128 weight rows fit
+// Whether the GEMM serves a call: from an average of 20 rows an expert on, where the scales of 128 weight rows fit
 // LDS beside x, a launch holds the tiles (2^32 threads) and x is addressed in 32 bits.
 inline bool gemm_path(const MoeArgs& a) {
     const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1;
-    return a.tokens * a.top_k >= (int64_t)24 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
+    return a.tokens * a.top_k >= (int64_t)20 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
            gemm_lds_bytes(a.hidden, a.group) <= kGemmMaxLds;
 }
 
