@@ -568,18 +568,13 @@ qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, i
  * that follow each other to the largest of them and drop what lies below 2^-13 of its power of two: for normally
  * distributed values 1.4e-5 of y, a fifteenth of float16's rounding. All other calls lose nothing that float32
  * holds.
- *   workspace: a device buffer of at least qaff_block_qmm_workspace_size(m, n, k) bytes, 16-byte aligned,
- *   which the call overwrites (float32 partial sums where few rows split K, joined in a fixed order); may be
- *   null where that size is 0. Results are deterministic.
+ * Results are deterministic.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown y_dtype, null or misaligned pointers (scales 4
- * bytes, y its element size), a short workspace; UNSUPPORTED for m of 2^31 or more, n of 2^28 or more, k above 2^18.
+ * bytes, y its element size); UNSUPPORTED for m of 2^31 or more, n of 2^28 or more, k above 2^18.
  */
 qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, const uint8_t* w,
-                           const float* w_scales, int64_t n, int64_t k, void* workspace,
-                           size_t workspace_bytes, void* y, qaff_dtype y_dtype, hipStream_t stream);
-
-/* Bytes of workspace qaff_block_qmm needs for these sizes (0: none). */
-size_t qaff_block_qmm_workspace_size(int64_t m, int64_t n, int64_t k);
+                           const float* w_scales, int64_t n, int64_t k, void* y, qaff_dtype y_dtype,
+                           hipStream_t stream);
 
 /* Text for the last non-OK status returned on the calling thread ("" if none). The pointer stays
  * valid until the thread's next qaff call. */

@@ -28,7 +28,7 @@ EXPORTS = ("qaff_dequantize", "qaff_qmm", "qaff_qmm_ex", "qaff_dequant_rows", "q
            "qaff_dequantize_typed", "qaff_qmm_typed", "qaff_quantize_typed", "qaff_gather_qmm_typed",
            "qaff_qmm_nt_typed", "qaff_paged_plan", "qaff_rope_append", "qaff_paged_attention",
            "qaff_paged_attention_workspace_size", "qaff_moe_route", "qaff_moe_ffn", "qaff_moe_ffn_workspace_size",
-           "qaff_block_quantize", "qaff_block_qmm", "qaff_block_qmm_workspace_size")
+           "qaff_block_quantize", "qaff_block_qmm")
 
 ABI_VERSION = 1
 
@@ -95,9 +95,7 @@ def load() -> ctypes.CDLL:
     lib.qaff_moe_ffn_workspace_size.argtypes = [i64, i64, i64, i64, i64, i32, i32]
     lib.qaff_moe_ffn_workspace_size.restype = size
     lib.qaff_block_quantize.argtypes = [vp, ctypes.c_int, i64, i64, i64, i32, vp, vp, vp]
-    lib.qaff_block_qmm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, size, vp, ctypes.c_int, vp]
-    lib.qaff_block_qmm_workspace_size.argtypes = [i64, i64, i64]
-    lib.qaff_block_qmm_workspace_size.restype = size
+    lib.qaff_block_qmm.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, ctypes.c_int, vp]
     for f in (lib.qaff_moe_route, lib.qaff_moe_ffn, lib.qaff_block_quantize, lib.qaff_block_qmm,
               lib.qaff_paged_plan, lib.qaff_rope_append, lib.qaff_paged_attention, lib.qaff_dequantize, lib.qaff_qmm, lib.qaff_qmm_ex, lib.qaff_dequant_rows,
               lib.qaff_gemv_gate_up, lib.qaff_gemv_silu_gate, lib.qaff_gather_qmm, lib.qaff_gather_qmm_ex,

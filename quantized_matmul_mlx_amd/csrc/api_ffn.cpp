@@ -178,14 +178,8 @@ qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, i
     return after_launch(op, qaff::launch_block_quantize(a, block_rows == 1, stream), stream);
 }
 
-size_t qaff_block_qmm_workspace_size(int64_t m, int64_t n, int64_t k) {
-    if (m <= 0 || n <= 0 || k <= 0 || m >= k2G || n >= 1LL << 28 || k > kMaxBlockK) return 0;
-    return qaff::block_qmm_workspace(m, n, k);
-}
-
 qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, const uint8_t* w, const float* w_scales,
-                           int64_t n, int64_t k, void* workspace, size_t workspace_bytes, void* y, qaff_dtype y_dtype,
-                           hipStream_t stream) {
+                           int64_t n, int64_t k, void* y, qaff_dtype y_dtype, hipStream_t stream) {
     const char* op = "qaff_block_qmm";
     qaff::set_error("");
     if (!any_dtype(y_dtype)) return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: unknown dtype %d", op, (int)y_dtype);
@@ -202,13 +196,6 @@ qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, c
         if (st == QAFF_OK) st = check_ptr(op, "w_scales", w_scales, 4);
     }
     if (st != QAFF_OK) return st;
-    const size_t need = k > 0 ? qaff::block_qmm_workspace(m, n, k) : 0;
-    if (need > 0) {
-        st = check_ptr(op, "workspace", workspace, 16);
-        if (st != QAFF_OK) return st;
-        if (workspace_bytes < need)
-            return fail(QAFF_ERR_INVALID_ARGUMENT, "%s: a workspace of %zu bytes, %zu needed", op, workspace_bytes, need);
-    }
     qaff::BlockQmmArgs a{};
     a.x = x;
     a.w = w;
@@ -219,7 +206,6 @@ qaff_status qaff_block_qmm(const uint8_t* x, const float* x_scales, int64_t m, c
     a.n = n;
     a.k = k;
     a.dtype = (int)y_dtype;
-    a.workspace = static_cast<float*>(workspace);
     return after_launch(op, qaff::launch_block_qmm(a, stream), stream);
 }
 

@@ -431,8 +431,6 @@ hipError_t launch_tiles(const BlockQmmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t block_qmm_workspace(int64_t, int64_t, int64_t) { return 0; }
-
 hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t stream) {
     const bool aligned = a.k > 0 && a.k % 16 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.w % 16 == 0;
     if (aligned && a.m > 64 && a.m * a.n < (int64_t)1 << 40) {

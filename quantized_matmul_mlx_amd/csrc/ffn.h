@@ -71,9 +71,7 @@ struct BlockQmmArgs {
     void* y;                          // [m, n]
     int64_t m, n, k;
     int dtype;                        // of y: 0 float32, 1 bf16, 2 float16
-    float* workspace;
 };
 hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t stream);
-size_t block_qmm_workspace(int64_t m, int64_t n, int64_t k);
 
 }  // namespace qaff

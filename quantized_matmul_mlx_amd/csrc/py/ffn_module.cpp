@@ -186,11 +186,8 @@ PyObject* block_qmm(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                     "of w), got " + shape_of(xs) + " and " + shape_of(ws));
         const Place place(x);
         const at::Tensor out = output_of(a[5], x, with_last(x, rows), type);
-        const size_t bytes = qaff_block_qmm_workspace_size(r.rows, rows, r.cols);
-        at::Tensor work;
-        if (bytes) work = empty({(int64_t)bytes}, x, at::kByte);
         check(qaff_block_qmm(ptr<uint8_t>(x), ptr<float>(xs), r.rows, ptr<uint8_t>(w), ptr<float>(ws), rows, r.cols,
-                             bytes ? work.data_ptr() : nullptr, bytes, ptr<void>(out), code_of(type), place.stream));
+                             ptr<void>(out), code_of(type), place.stream));
         return THPVariable_Wrap(out);
     });
 }

@@ -29,7 +29,6 @@ hipError_t launch_block_quantize(const BlockQuantArgs& a, bool r, hipStream_t) {
     return quant = a, by_row = r, ++launches, result;
 }
 hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t) { return qmm = a, ++launches, result; }
-size_t block_qmm_workspace(int64_t m, int64_t, int64_t) { return m > 100 ? 64 : 0; }
 }  // namespace qaff
 hipError_t hipStreamSynchronize(hipStream_t) { return hipSuccess; }
 const char* hipGetErrorString(hipError_t) { return "stub"; }
@@ -91,20 +90,17 @@ int main() {
         CHECK(quantize(v, 200, 200, 1) != QAFF_OK && quantize(5, v, v, 1) != QAFF_OK && quantize(5, 200, v, 1) != QAFF_OK);
     CHECK(launches == done);
 
-    auto product = [&](int64_t m, int64_t n, int64_t k, void* work, size_t bytes) {
-        return qaff_block_qmm(u8, f32, m, u8, f32, n, k, work, bytes, p, QAFF_F32, nullptr);
+    auto product = [&](int64_t m, int64_t n, int64_t k) {
+        return qaff_block_qmm(u8, f32, m, u8, f32, n, k, p, QAFF_F32, nullptr);
     };
-    CHECK(product(3, 64, 256, nullptr, 0) == QAFF_OK && launches == ++done && qmm.m == 3 && qmm.n == 64 && qmm.k == 256);
-    CHECK(product(101, 64, 256, nullptr, 0) == QAFF_ERR_INVALID_ARGUMENT && product(101, 64, 256, p, 63) == QAFF_ERR_INVALID_ARGUMENT);
-    CHECK(product(101, 64, 256, p, 64) == QAFF_OK && launches == ++done && qmm.workspace == f32);
-    for (int64_t v : {big, low}) {
-        CHECK(product(v, 64, 256, p, 64) != QAFF_OK && product(3, v, 256, p, 64) != QAFF_OK && product(3, 64, v, p, 64) != QAFF_OK);
-        CHECK(qaff_block_qmm_workspace_size(v, v, v) == 0);
-    }
+    CHECK(product(3, 64, 256) == QAFF_OK && launches == ++done && qmm.m == 3 && qmm.n == 64 && qmm.k == 256 && qmm.y == p);
+    CHECK(product(3, 64, 0) == QAFF_OK && launches == ++done && qmm.k == 0);
+    for (int64_t v : {big, low})
+        CHECK(product(v, 64, 256) != QAFF_OK && product(3, v, 256) != QAFF_OK && product(3, 64, v) != QAFF_OK);
     CHECK(launches == done);
 
     result = hipErrorLaunchFailure;
-    CHECK(product(3, 64, 256, nullptr, 0) == QAFF_ERR_DEVICE && error.find("stub") != std::string::npos);
+    CHECK(product(3, 64, 256) == QAFF_ERR_DEVICE && error.find("stub") != std::string::npos);
     result = hipErrorInvalidConfiguration;
     CHECK(quantize(5, 200, 256, 1) == QAFF_ERR_UNSUPPORTED);
     std::printf("all checks passed\n");

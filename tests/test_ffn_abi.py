@@ -42,7 +42,7 @@ def quantize(lib, **kw):
 
 
 def product(lib, **kw):
-    a = dict(x=A, xs=A, m=3, w=A, ws=A, n=64, k=256, work=A, work_bytes=1 << 40, y=A, dtype=_lib.QAFF_BF16)
+    a = dict(x=A, xs=A, m=3, w=A, ws=A, n=64, k=256, y=A, dtype=_lib.QAFF_BF16)
     assert not set(kw) - set(a)
     return lib.qaff_block_qmm(*{**a, **kw}.values(), None)
 
