@@ -563,11 +563,11 @@ qaff_status qaff_block_quantize(const void* x, qaff_dtype dtype, int64_t rows, i
  *   y[m, n] = sum_j x_scales[m, j] w_scales[n / 128, j] sum_{128 j <= i < 128 (j + 1)} x[m, i] w[n, i]
  *   x uint8 [m, k], x_scales float32 [m, ceil(k / 128)]; w uint8 [n, k], w_scales float32
  *   [ceil(n / 128), ceil(k / 128)]; y [m, n] of y_dtype (float32, bf16 or float16).
- * Sums are float32, y is rounded once at the end. k == 0 writes zeros. From 65 rows of x on, 16-byte aligned rows of
- * x and w (k a multiple of 16) with a 16-bit y take the 8-bit matrix instructions, which align each eight products
- * that follow each other to the largest of them and drop what lies below 2^-13 of its power of two: for normally
- * distributed values 1.4e-5 of y, a fifteenth of float16's rounding. All other calls lose nothing that float32
- * holds.
+ * Sums are float32, y is rounded once at the end. k == 0 writes zeros. From 65 rows of x on (from 17 where n / 64 is
+ * half the compute units or more), 16-byte aligned rows of x and w (k a multiple of 16) with a 16-bit y take the
+ * 8-bit matrix instructions, which align each eight products that follow each other to the largest of them and drop
+ * what lies below 2^-13 of its power of two: for normally distributed values 1.4e-5 of y, a fifteenth of float16's
+ * rounding. All other calls lose nothing that float32 holds.
  * Results are deterministic.
  * Errors: INVALID_ARGUMENT for negative sizes, an unknown y_dtype, null or misaligned pointers (scales 4
  * bytes, y its element size); UNSUPPORTED for m of 2^31 or more, n of 2^28 or more, k above 2^18.

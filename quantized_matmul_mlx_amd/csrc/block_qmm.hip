@@ -209,10 +209,11 @@ hipError_t launch_few_rows(const BlockQmmArgs& a, hipStream_t stream) {
 
 // ---- tiles -----------------------------------------------------------------------------------------
 //
-// Many rows: a workgroup of 4 waves has 16 MT x 64 NT outputs, wave w the columns 16 NT w of them and all rows.
+// More rows: a workgroup has 16 MT x 16 WAVES NT outputs, wave w the columns 16 NT w of them and all rows. With SPLIT
+// it has that many sets of waves, each for a part of K with stages of its own; their sums meet in LDS in the end.
 //  * w goes straight from memory into the products' operands, three blocks of K ahead in registers: no
 //    wave shares its rows, and LDS, which the rows of x already fill, carries it not.
-//  * x goes through LDS, two blocks at a time (16-byte pieces, swapped within a row by half the row's
+//  * x goes through LDS, three blocks of it there at a time (16-byte pieces, swapped within a row by half the row's
 //    number so that 16 rows at one offset fall on distinct banks), with the products of its and w's scales beside it.
 //  * One v_mfma_f32_16x16x128_f8f6f4 is a block of K for 16 x 16 outputs (32 cycles); its four results a
 //    lane enter the totals with the scales by four multiply-adds (16 cycles), those of the previous 16 rows
@@ -227,21 +228,32 @@ __device__ __forceinline__ f32x4 mfma_f8(i32x8 a, i32x8 b) {
 template <int T> struct Type { static constexpr int value = T; };
 
 // TAIL: k is not a multiple of 128 (but of 16): the last block's pieces past the end are 0 in w.
-template <int WAVES, int MT, int NT, bool EXACT, bool TAIL>
-__global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, int tiles_m, int tiles_n) {
+template <int WAVES, int MT, int NT, int SPLIT, bool EXACT, bool TAIL>
+__global__ __launch_bounds__(64 * WAVES * SPLIT) void qmm_tile_kernel(BlockQmmArgs a, int tiles_m, int tiles_n) {
     constexpr int kThreads = 64 * WAVES, kRows = 16 * MT, kCols = 16 * WAVES * NT;
     constexpr int kPieces = kRows * 8 / kThreads;  // pieces of x a thread and block
-    constexpr int kScales = kCols / kBlock;        // blocks of 128 columns
+    constexpr int kScales = (kCols + kBlock - 1) / kBlock;  // blocks of 128 columns
     constexpr int kPanel = kThreads / kRows;       // blocks of K whose scales are loaded together
     constexpr int kStages = 3;
-    __shared__ __attribute__((aligned(16))) uint8_t xl[kStages][kRows * kBlock];
-    __shared__ __attribute__((aligned(16))) float sl[2][kPanel][kScales][kRows];
-    const int tid = threadIdx.x, lane = tid & 63;
+    __shared__ __attribute__((aligned(16))) uint8_t x_all[SPLIT][kStages][kRows * kBlock];
+    __shared__ __attribute__((aligned(16))) float s_all[SPLIT][2][kPanel][kScales][kRows];
+    const int part = SPLIT > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads) : 0;
+    auto& xl = x_all[part];
+    auto& sl = s_all[part];
+    const int tid = threadIdx.x % kThreads, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
     const int64_t m0 = (int64_t)tm * kRows, n0 = (int64_t)tn * kCols;
     const int kb = (int)((a.k + kBlock - 1) / kBlock);
+    // This part's blocks: `own` from b0 on (at least one; `turns` count), in the order at(0), at(1), ...; past them it
+    // repeats others, whose scales are stored as 0.
+    const int turns = (kb + SPLIT - 1) / SPLIT, b0 = min(part * turns, kb - 1), count = min(turns, kb - part * turns);
+    const int own = max(count, 1), first = SPLIT > 1 ? (int)((uint32_t)tn * 5u % (uint32_t)own) : 0;
+    auto at = [&](int b) {
+        const int i = b + first;
+        return b0 + min(i < own ? i : i - own, own - 1);
+    };
 
     // this thread's pieces of x: row and place in LDS; its scales: row tid % kRows, block tid / kRows of a panel
     const uint8_t* xp[kPieces];
@@ -265,16 +277,15 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
     struct Scales {
         float x, w[kScales];
     };
-    // Blocks past the last one repeat it (their scales are stored as 0).
     auto load_x = [&](Ahead& s, int b) {
-        b = min(b, kb - 1);
+        b = at(b);
         const int left = TAIL ? (int)min(a.k - (int64_t)b * kBlock, (int64_t)kBlock) : kBlock;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)  // a piece past the row's end repeats the last one: w is 0 there
             s.x[i] = *reinterpret_cast<const u32x4a*>(xp[i] + (int64_t)b * kBlock + min(16 * (tid & 7), left - 16));
     };
     auto load_w = [&](Ahead& s, int b) {
-        b = min(b, kb - 1);
+        b = at(b);
         const int left = TAIL ? (int)min(a.k - (int64_t)b * kBlock, (int64_t)kBlock) : kBlock;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -283,7 +294,7 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
         }
     };
     auto load_scales = [&](Scales& s, int panel) {
-        const int b = min(panel * kPanel + scale_block, kb - 1);
+        const int b = at(panel * kPanel + scale_block);
         s.x = xsp[b];
 #pragma unroll
         for (int i = 0; i < kScales; ++i) s.w[i] = a.w_scales[min(n0 / kBlock + i, (a.n - 1) / kBlock) * kb + b];
@@ -291,12 +302,12 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
     auto store_scales = [&](const Scales& s, int panel) {
 #pragma unroll
         for (int i = 0; i < kScales; ++i)
-            sl[panel & 1][scale_block][i][scale_row] = panel * kPanel + scale_block < kb ? s.x * s.w[i] : 0.f;
+            sl[panel & 1][scale_block][i][scale_row] = panel * kPanel + scale_block < count ? s.x * s.w[i] : 0.f;
     };
     auto operand = [&](const Ahead& s, int j, int b) {
         u32x4a lo = s.lo[j], hi = s.hi[j];
         if constexpr (TAIL) {
-            const int64_t left = a.k - (int64_t)b * kBlock;
+            const int64_t left = a.k - (int64_t)at(b) * kBlock;
             if (16 * g >= left) lo = u32x4a{0u, 0u, 0u, 0u};
             if (64 + 16 * g >= left) hi = u32x4a{0u, 0u, 0u, 0u};
         }
@@ -375,7 +386,7 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
     __syncthreads();
     read(0, 0, 0);
     read_scale(0, 0, 0);
-    for (int b = 0; b < kb; b += 3) {
+    for (int b = 0; b < turns; b += 3) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             // After this barrier nobody reads block b + i - 1 any more, whose place block b + i + 2 takes; block
@@ -395,6 +406,25 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[MT - 1][j][v] = __builtin_fmaf(scale[1][v], d[1][j][v], acc[MT - 1][j][v]);
+    if constexpr (SPLIT > 1) {  // the parts' sums, in order
+        static_assert(sizeof(x_all) >= (SPLIT - 1) * WAVES * MT * NT * 1024, "");
+        f32x4* red = reinterpret_cast<f32x4*>(&x_all[0][0][0]);
+        auto place = [&](int p, int i, int j) { return (((p - 1) * WAVES + wave) * MT * NT + i * NT + j) * 64 + lane; };
+        __syncthreads();  // nobody reads x any more
+        if (part > 0)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) red[place(part, i, j)] = acc[i][j];
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int p = 1; p < SPLIT; ++p)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[i][j] += red[place(p, i, j)];
+    }
     auto store = [&](auto type) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -414,17 +444,17 @@ __global__ __launch_bounds__(64 * WAVES) void qmm_tile_kernel(BlockQmmArgs a, in
     else store(Type<2>());
 }
 
-template <int WAVES, int MT, int NT>
+template <int WAVES, int MT, int NT, int SPLIT>
 hipError_t launch_tiles(const BlockQmmArgs& a, hipStream_t stream) {
     const int tiles_m = (int)((a.m + 16 * MT - 1) / (16 * MT));
     const int tiles_n = (int)((a.n + 16 * WAVES * NT - 1) / (16 * WAVES * NT));
-    const dim3 grid((unsigned)tiles_m * (unsigned)tiles_n), block(64 * WAVES);
+    const dim3 grid((unsigned)tiles_m * (unsigned)tiles_n), block(64 * WAVES * SPLIT);
     if (a.k % kBlock) {
-        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, true, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
-        else qmm_tile_kernel<WAVES, MT, NT, false, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, SPLIT, true, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        else qmm_tile_kernel<WAVES, MT, NT, SPLIT, false, true><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
     } else {
-        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, true, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
-        else qmm_tile_kernel<WAVES, MT, NT, false, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        if (a.dtype == 0) qmm_tile_kernel<WAVES, MT, NT, SPLIT, true, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
+        else qmm_tile_kernel<WAVES, MT, NT, SPLIT, false, false><<<grid, block, 0, stream>>>(a, tiles_m, tiles_n);
     }
     return hipGetLastError();
 }
@@ -433,10 +463,19 @@ hipError_t launch_tiles(const BlockQmmArgs& a, hipStream_t stream) {
 
 hipError_t launch_block_qmm(const BlockQmmArgs& a, hipStream_t stream) {
     const bool aligned = a.k > 0 && a.k % 16 == 0 && (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.w % 16 == 0;
-    if (aligned && a.m > 64 && a.m * a.n < (int64_t)1 << 40) {
-        const int64_t big = ((a.m + 127) / 128) * ((a.n + 255) / 256);
-        if (big >= device_cu_count() * 3 / 4) return launch_tiles<8, 8, 2>(a, stream);
-        return launch_tiles<4, 4, 2>(a, stream);
+    const int64_t cus = device_cu_count();
+    auto tiles = [&](int rows, int cols) { return ((a.m + rows - 1) / rows) * ((a.n + cols - 1) / cols); };
+    // Tiles of 128 x 256 where half the compute units get one ([1280, 4096] x [4096, 4096], 160 of them: 48 us against 66
+    // with 64 x 128; [512, 4096], 64 of them, would leave most units idle: 25 with 64 x 128). Below that 64 x 64 with K
+    // split where each unit gets one at most, and 64 x 128 otherwise ([256, 4096] x [4096, 4096], 256 tiles of 64 x 64:
+    // 18.6 against 22; [512, 4096], 512 of them: 31 against 25). From 17 rows of x on where half the units get a tile of
+    // 64 x 64: [61, 4096] x [14336, 4096] 17 against 29.7 us with the kernel for few rows, [64, 8192] x [8192, 8192]
+    // 25.9 against 28, but [64, 4096] x [4096, 4096] 15.9 against 13.8; from 65 rows on always, since that kernel
+    // would read w more than once.
+    if (aligned && a.m > 16 && a.m * a.n < (int64_t)1 << 40) {
+        if (a.m > 64 && tiles(128, 256) >= cus / 2) return launch_tiles<8, 8, 2, 1>(a, stream);
+        if (tiles(64, 64) > cus) return launch_tiles<4, 4, 2, 1>(a, stream);
+        if (a.m > 64 || tiles(64, 64) >= cus / 2) return launch_tiles<4, 4, 1, 2>(a, stream);
     }
     const int64_t kb = (a.k + kBlock - 1) / kBlock;
     if (a.m > 32 && few_lds(4, 4, kb) <= kFewMaxLds) return launch_few_rows<4>(a, stream);

@@ -210,6 +210,28 @@ def test_product_calls(m, k):
     assert got[:, n - 1].isnan().all() and torch.equal(got[:, :n - 1], y[:, :n - 1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("m,n,k", [(17, 8200, 16), (20, 8193, 128), (33, 8200, 272), (61, 9000, 384), (64, 16385, 400), (18, 20000, 640),
+                                   (65, 200, 144), (66, 129, 896), (128, 300, 1920), (70, 4096, 256), (768, 600, 528)])
+def test_product_split(dtype, m, n, k):
+    """Few rows against wide weights, and small products: K in two parts, down to one block and to a part without any."""
+    (x, xs), (w, ws) = product_inputs(gen_of("split", m, n, k), m, n, k)
+    banner(f"product {m} x {n} x {k} {dtype}")
+    y = qaff.block_qmm(x, xs, w, ws, out_dtype=dtype)
+    want, bound = ref.product(x, xs, w, ws, dtype, eights=dtype != F32)
+    check(y, want, bound, f"{m} x {n} x {k}")
+    rms = ((y.double() - want).norm() / want.norm()).item()
+    assert rms <= ref.HALF[dtype] * 0.58 + 3e-5
+    nan = x.clone()
+    nan.view(torch.uint8)[m - 1, k - 1] = 0x7F
+    got = qaff.block_qmm(nan, xs, w, ws, out_dtype=dtype)
+    assert got[m - 1].isnan().all() and torch.equal(got[:m - 1], y[:m - 1])
+    scales = xs.clone()
+    scales[1, 0] = float("inf")
+    got = qaff.block_qmm(x, scales, w, ws, out_dtype=dtype)
+    assert not got[1].isfinite().any() and torch.equal(got[2:], y[2:]) and torch.equal(got[0], y[0])
+
+
 def test_product_shapes():
     (x, xs), (w, ws) = product_inputs(gen_of("shapes"), 6, 130, 300)
     y = qaff.block_qmm(x, xs, w, ws)
