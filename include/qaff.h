@@ -521,8 +521,11 @@ qaff_status qaff_moe_route(const void* logits, qaff_dtype dtype, int64_t tokens,
  *   multiples of group_size.
  *   workspace: a device buffer of at least qaff_moe_ffn_workspace_size(...) bytes, 16-byte aligned, which
  *   the call overwrites. y may be resid.
- * Sums are float32, silu(g) * u is rounded to dtype for its product with D, y is rounded once at the end.
- * Results are deterministic.
+ * Sums are float32, y is rounded once at the end, and results are deterministic. Below an average of 20 pairs an
+ * expert the weights' codes, scales and biases enter exactly and silu(g) * u is rounded to dtype for its product with
+ * D (in float16 it is infinite from 65520 on); from there on, up to 2^31 elements of x, weights, x and silu(g) * u are
+ * rounded to 11 bits, with a power of two of their own for each row of a weight and of x and each 16 columns of
+ * silu(g) * u (what lies below 2^-40 of its row's largest counts as 0).
  * Errors: INVALID_ARGUMENT for negative sizes, a dtype other than bf16 and float16, a bad group size, width
  * or hidden that is not a multiple of it, null or misaligned pointers (2 bytes; 4 for codes, chosen and
  * weights), a short workspace; UNSUPPORTED for a bit width not listed above, width or hidden above 32768,

@@ -12,7 +12,7 @@
 // multiply-add forms s c + b. To stay inside float16's range every row of a weight has a power of two of its
 // own, found when a workgroup takes its scales and biases into LDS, and so has every row of x (bf16 values
 // keep their 8 bits) and every 16 columns of a row of h. Against float64, weights rounded to 8 bits instead
-// would cost 1.5 times the rounding of y; these cost a hundredth.
+// would cost 1.5 times the rounding of y; these cost a hundredth. h has 11 bits and so loses no more.
 //
 // A workgroup of 4 waves has 128 rows of a weight, 32 a wave, dequantized once in registers by the wave that
 // multiplies them, against up to 6 x 32 rows of x from LDS (only as many as there are). Two workgroups share a
@@ -639,11 +639,14 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     return f16 ? launch_combine<true>(a, g.d, stream) : launch_combine<false>(a, g.d, stream);
 }
 
-// Whether the GEMM serves a call: from an average of 20 rows an expert on, where the scales of 128 weight rows fit
-// LDS beside x, a launch holds the tiles (2^32 threads) and x is addressed in 32 bits.
+// Whether the GEMM serves a call: from an average of 20 rows an expert on (128 x [768, 2048] in 4 bits, 8 experts a token:
+// 376 tokens, 23.5 rows, take 169 us with it and 218 with the kernels for few rows; at 256 tokens, 16 rows, one pass
+// of those, they take 162), where the scales of 128 weight rows fit LDS beside x, a launch holds the tiles (2^32 threads)
+// and x is addressed in 32 bits.
 inline bool gemm_path(const MoeArgs& a) {
     const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1;
-    return a.tokens * a.top_k >= (int64_t)20 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 && gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
+    return a.tokens * a.top_k >= (int64_t)20 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 &&
+           gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
            gemm_lds_bytes(a.hidden, a.group) <= kGemmMaxLds;
 }
 
