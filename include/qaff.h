@@ -522,7 +522,7 @@ qaff_status qaff_moe_route(const void* logits, qaff_dtype dtype, int64_t tokens,
  *   workspace: a device buffer of at least qaff_moe_ffn_workspace_size(...) bytes, 16-byte aligned, which
  *   the call overwrites. y may be resid.
  * Sums are float32, y is rounded once at the end, and results are deterministic. Below an average of 20 pairs an
- * expert the weights' codes, scales and biases enter exactly and silu(g) * u is rounded to dtype for its product with
+ * expert (fewer where width or hidden is above 4472) the weights' codes, scales and biases enter exactly and silu(g) * u is rounded to dtype for its product with
  * D (in float16 it is infinite from 65520 on); from there on, up to 2^31 elements of x, weights, x and silu(g) * u are
  * rounded to 11 bits, with a power of two of their own for each row of a weight and of x and each 16 columns of
  * silu(g) * u (what lies below 2^-40 of its row's largest counts as 0).

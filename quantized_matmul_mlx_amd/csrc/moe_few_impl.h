@@ -10,6 +10,8 @@
 //    each group's scale and bias are applied to the group's sums:
 //      sum x (s c + b) = s sum x (B + c) + (b - B s) sum x.
 //    No weight is rounded, and the sums of x come from LDS, where they are formed once a workgroup.
+//    Measured (kernels alone): 64 tokens through 8 of 128 x [768, 2048], 4 bits: gate and up 58 us, down 34, combine 6.7,
+//    340 MB in all, 3.5 TB/s; one token, each pair alone: 7.9 and 7.4 us.
 //  * h = silu(g) u is rounded to the type of x: the matrix instructions take 16-bit operands of one type, and x and
 //    the code operands B + c have that one. d, its sum over a token and both products' sums are float32.
 //  * v_mfma_f32_16x16x32: a lane loads a whole block of 32 codes (16 bytes at 4 bits) of weight row

@@ -14,8 +14,13 @@
 // keep their 8 bits) and every 16 columns of a row of h. Against float64, weights rounded to 8 bits instead
 // would cost 1.5 times the rounding of y; these cost a hundredth. h has 11 bits and so loses no more.
 //
+// Measured (kernels alone): 2048 tokens through 8 of 128 x [768, 2048], 4 bits: sort 12.4 us, gate and up 158, down 125,
+// combine 24, 155 GFLOP in all; 512 tokens through 2 of 8 x [14336, 4096]: 434 and 340 us,
+// where the kernels for few rows take 3.8 ms. Bound by
+// what surrounds the products of a tile: 143 of 189 us stayed when all loads and dequantization were left out.
+//
 // A workgroup of 4 waves has 128 rows of a weight, 32 a wave, dequantized once in registers by the wave that
-// multiplies them, against up to 6 x 32 rows of x from LDS (only as many as there are). Two workgroups share a
+// multiplies them, against up to 5 x 32 rows of x from LDS (only as many as there are). Two workgroups share a
 // compute unit, so that one's products cover the other's loads. v_mfma_f32_32x32x16_f16: lane l supplies row
 // l % 32 of x and of the weight, 8 values at k-slot l / 32; result v of lane l is D[8 (v / 4) + 4 (l / 32)
 // + v % 4][l % 32].
@@ -202,8 +207,16 @@ __device__ __forceinline__ uint32_t weight_word(const uint32_t (&w)[BITS], int j
 // ---- the GEMM -----------------------------------------------------------------------------------------
 
 // LDS: three stages of x, then the scales and biases of the 128 weight rows.
-inline int gemm_lds_bytes(int k, int group) { return kStages * kStageBytes + 128 * (k / group + 1) * 4; }
-constexpr int kGemmMaxLds = 158 * 1024;
+// Scales and biases are there for a window of K: all of a row's up to 32 groups, and otherwise those of window_units
+// units and of the unit behind them (whose first is read one step early), so that two workgroups fit a compute unit.
+constexpr int kWindow = 32;
+__host__ __device__ constexpr int window_units(int gshift) { return 3 * (((kWindow >> (2 - gshift)) - 1) / 3); }  // 6, 15, 30
+__host__ __device__ constexpr int window_groups(int gpr, int gshift) {
+    return gpr <= kWindow ? gpr : (4 * window_units(gshift) + 4) >> gshift;
+}
+inline int gemm_lds_bytes(int k, int gshift) {
+    return kStages * kStageBytes + 128 * (window_groups(k >> (5 + gshift), gshift) + 1) * 4;
+}
 
 // The largest magnitude of the 16 lanes of a row.
 __device__ __forceinline__ float row_max(float v) {
@@ -229,10 +242,18 @@ __device__ __forceinline__ int most_of(const uint8_t* p, int n) {
     return (int)m;
 }
 
+// A group's scale and bias as they lie in the window.
+__device__ __forceinline__ uint32_t to_window(uint32_t s, uint32_t b, int up, bool f16) {
+    auto value = [&](uint32_t v) { return f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
+    return pack_half2<true>(ldexpf(value(s), up), ldexpf(value(b), up - 24));
+}
+
 // What a workgroup finds before its loop.
 struct GemmTile {
     const uint32_t* pw;      // this lane's weight row
-    uint32_t* sb;            // its scales and biases in LDS
+    uint32_t* sb;            // the window of its scales and biases in LDS
+    const uint16_t *sp, *bp; // and all of them
+    int up;                  // scales are times 2^up there, biases 2^(up - 24)
     uint8_t* xl;
     const uint16_t* x;       // a.x, DOWN: from the tile's first row on
     const uint8_t* exps;     // DOWN: the exponents, from the tile's first row on
@@ -293,8 +314,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
 #pragma unroll
         for (int s = 0; s < 2; ++s) load_block<BITS>(c.pw + min(4 * min(u, units - 1) + 2 * h + s, kb - 1) * BITS, w[s]);
     };
+    int base = 0;  // the window's first group
     auto group_at = [&](int t) {
-        return group_of(c.sb[min(((t >> 1) * 4 + 2 * h + (t & 1)) >> a.gshift, gpr - 1)]);
+        return group_of(c.sb[min(((t >> 1) * 4 + 2 * h + (t & 1)) >> a.gshift, gpr - 1) - base]);
     };
     f32x16 acc[T];
 #pragma unroll
@@ -375,7 +397,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, const GemmTile& c, 
         step(2 * u, stage, w[0], w[1], g, xa);
         step(2 * u + 1, (stage + 1) % kStages, w[1], follow[0], g, xb);
     };
+    int move = gpr > kWindow ? window_units(a.gshift) : units;  // the unit from which on the next window is read
     for (int u = 0;; u += 3) {  // six steps: the stages and the weights' registers turn
+        if (u == move) {
+            base = (4 * u) >> a.gshift;
+            move += window_units(a.gshift);
+            const int there = min(window_groups(gpr, a.gshift), gpr - base);
+            for (int i = h; i < there; i += 2) c.sb[i] = to_window(c.sp[base + i], c.bp[base + i], c.up, a.f16);
+            __builtin_amdgcn_wave_barrier();  // the row's other lanes read it
+        }
         unit(u, 0, w0, w1, w2);
         if (u + 1 >= units) break;
         unit(u + 1, 2, w1, w2, w0);
@@ -482,7 +512,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
     c.row0 = where[1];
     c.rows = min(kTileM, where[2] - c.row0);
     c.tn = tn;
-    const int kb = a.k / 32, gpr = kb >> a.gshift, spitch = gpr + 1;
+    const int kb = a.k / 32, gpr = kb >> a.gshift, window = window_groups(gpr, a.gshift);
 
     // rows of x: where they are and their power of two
     for (int i = tid; i < kTileM; i += kGemmThreads) {
@@ -508,38 +538,50 @@ __global__ __launch_bounds__(kGemmThreads, 2) void moe_gemm_kernel(GemmArgs a) {
 
     // Scales and biases to LDS, times the power of two of the row: the largest scale 2^24 lies in [2^14, 2^15). First as
     // they are, eight groups a load (the lanes of a row take eights in turn), then changed where they lie.
-    const uint16_t* sp = W.scales + wr * gpr;
-    const uint16_t* bp = W.biases + wr * gpr;
-    c.sb = reinterpret_cast<uint32_t*>(smem + kStages * kStageBytes) + (32 * wave + r) * spitch;
-    for (int g = 8 * h; g < gpr; g += 16) {
-        if (g + 8 <= gpr) {
-            const u32x4h sv = *reinterpret_cast<const u32x4h*>(sp + g), bv = *reinterpret_cast<const u32x4h*>(bp + g);
+    c.sp = W.scales + wr * gpr;
+    c.bp = W.biases + wr * gpr;
+    c.sb = reinterpret_cast<uint32_t*>(smem + kStages * kStageBytes) + (32 * wave + r) * (window + 1);
+    auto value = [&](uint32_t v) { return a.f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
+    float top = 0.f;
+    auto see = [&](uint32_t v) { top = fmaxf(top, fmaxf(fabsf(value(v)), fabsf(value(v >> 16)) * 0x1p-20f)); };
+    auto both = [](uint32_t s, uint32_t b) { return (s & 0xffffu) | b << 16; };
+    for (int g = 8 * h; g < window; g += 16) {
+        if (g + 8 <= window) {
+            const u32x4h sv = *reinterpret_cast<const u32x4h*>(c.sp + g), bv = *reinterpret_cast<const u32x4h*>(c.bp + g);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 c.sb[g + 2 * q] = __builtin_amdgcn_perm(bv[q], sv[q], 0x05040100u);
                 c.sb[g + 2 * q + 1] = __builtin_amdgcn_perm(bv[q], sv[q], 0x07060302u);
             }
         } else {
-            for (int q = g; q < gpr; ++q) c.sb[q] = (uint32_t)sp[q] | (uint32_t)bp[q] << 16;
+            for (int q = g; q < window; ++q) c.sb[q] = both(c.sp[q], c.bp[q]);
         }
     }
-    auto value = [&](uint32_t v) { return a.f16 ? half_to_f32<true>(v) : half_to_f32<false>(v); };
-    float top = 0.f;
-    for (int g0 = 8 * h; g0 < gpr; g0 += 16)
+    for (int g0 = 8 * h; g0 < window; g0 += 16)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint32_t v = c.sb[min(g0 + q, gpr - 1)];
-            top = fmaxf(top, fmaxf(fabsf(value(v)), fabsf(value(v >> 16)) * 0x1p-20f));
+        for (int q = 0; q < 8; ++q) see(c.sb[min(g0 + q, window - 1)]);
+    for (int g = window + 8 * h; g < gpr; g += 16) {  // those past the window count, too
+        if (g + 8 <= gpr) {
+            const u32x4h sv = *reinterpret_cast<const u32x4h*>(c.sp + g), bv = *reinterpret_cast<const u32x4h*>(c.bp + g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                see(both(sv[q], bv[q]));
+                see(both(sv[q] >> 16, bv[q] >> 16));
+            }
+        } else {
+            for (int q = g; q < gpr; ++q) see(both(c.sp[q], c.bp[q]));
         }
+    }
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     const int up = min(14 + 127 - max(min((int)(__float_as_uint(top) >> 23), 254), 1), 120);
-    for (int g0 = 8 * h; g0 < gpr; g0 += 16)
+    for (int g0 = 8 * h; g0 < window; g0 += 16)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (g0 + q < gpr) {
+            if (g0 + q < window) {
                 const uint32_t v = c.sb[g0 + q];
-                c.sb[g0 + q] = pack_half2<true>(ldexpf(value(v), up), ldexpf(value(v >> 16), up - 24));
+                c.sb[g0 + q] = to_window(v, v >> 16, up, a.f16);
             }
+    c.up = up;
     c.col_scale = ldexpf(1.f, 24 - up);
     c.xl = smem;
     c.x = DOWN ? a.x + (int64_t)c.row0 * pad_unit(a.k) : a.x;
@@ -623,7 +665,7 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     g.n = a.hidden;
     g.tiles_n = (a.hidden + 63) / 64;
     moe_gemm_kernel<BITS, false><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
-                                   gemm_lds_bytes(a.width, a.group), stream>>>(g);
+                                   gemm_lds_bytes(a.width, g.gshift), stream>>>(g);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     g.x = g.h;
@@ -633,21 +675,25 @@ hipError_t launch_gemm_path(const MoeArgs& a, bool f16, hipStream_t stream) {
     g.n = a.width;
     g.tiles_n = (a.width + 127) / 128;
     moe_gemm_kernel<BITS, true><<<dim3((unsigned)(tiles * g.tiles_n)), dim3(kGemmThreads),
-                                  gemm_lds_bytes(a.hidden, a.group), stream>>>(g);
+                                  gemm_lds_bytes(a.hidden, g.gshift), stream>>>(g);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return f16 ? launch_combine<true>(a, g.d, stream) : launch_combine<false>(a, g.d, stream);
 }
 
 // Whether the GEMM serves a call: from an average of 20 rows an expert on (128 x [768, 2048] in 4 bits, 8 experts a token:
-// 376 tokens, 23.5 rows, take 169 us with it and 218 with the kernels for few rows; at 256 tokens, 16 rows, one pass
-// of those, they take 162), where the scales of 128 weight rows fit LDS beside x, a launch holds the tiles (2^32 threads)
-// and x is addressed in 32 bits.
+// 376 tokens, 23.5 rows, take 171 us with it and 218 with the kernels for few rows; at 256 tokens, 16 rows, one pass
+// of those, they take 162), or of two of their passes where rows are so long that LDS holds fewer than 10 (8 x [8192, 8192]:
+// 80 tokens of 2 experts, 20 rows, 405 us with it, 64 tokens, 16 rows, 697 with the others in two passes;
+// 8 x [14336, 4096], four rows a pass: 64 tokens 387 against 685), as long as a launch holds the tiles (2^32 threads) and
+// x is addressed in 32 bits.
 inline bool gemm_path(const MoeArgs& a) {
-    const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1;
-    return a.tokens * a.top_k >= (int64_t)20 * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 &&
-           gemm_tiles(a) * widest < (int64_t)1 << 24 && gemm_lds_bytes(a.width, a.group) <= kGemmMaxLds &&
-           gemm_lds_bytes(a.hidden, a.group) <= kGemmMaxLds;
+    const int64_t widest = std::max(a.hidden / 64, a.width / 128) + 1, pairs = a.tokens * a.top_k;
+    const int64_t row = 2 * (int64_t)std::max(a.hidden, a.width) + 16;
+    int64_t pass = kTileRows;  // rows that LDS holds for the other kernels
+    while (pass > 1 && pass * row > 140 * 1024) pass /= 2;
+    return pairs >= std::min((int64_t)20, 2 * pass) * a.experts && a.tokens * pad_unit(a.width) < (int64_t)1 << 31 &&
+           gemm_tiles(a) * widest < (int64_t)1 << 24;
 }
 
 }  // namespace

@@ -155,6 +155,23 @@ def test_moe_scales_of_any_size(tokens, experts, top_k, bits):
     check(run_moe(i), want, bound, f"{bits} bits {tokens} tokens")
 
 
+@pytest.mark.parametrize("bits,group,hidden,width", [(4, 32, 1056, 1536), (4, 32, 1536, 1664), (2, 32, 3040, 1056), (6, 64, 2112, 3840),
+                                                     (4, 64, 4096, 2176), (8, 64, 3904, 2112), (3, 128, 4224, 7680), (5, 128, 7808, 4096)])
+@pytest.mark.parametrize("tokens", [70, 420])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_moe_many_rows_of_many_groups(bits, group, hidden, width, tokens, dtype):
+    """Rows of more groups than the GEMM holds at a time (32), up to and past the borders of what it holds; scales of
+    each row grow towards its end, where its largest stands."""
+    i = moe_inputs(gen_of("groups", bits, group, hidden, tokens), tokens, 3, 1, hidden, width, bits, group, dtype)
+    for name in ("gate", "up", "down"):
+        w, s, b = i[name]
+        grow = torch.linspace(-3, 1, s.shape[-1], device="cuda").exp2()
+        i[name] = (w, (s * grow).to(dtype), (b * grow).to(dtype))
+    banner(f"moe {bits} bits g{group} {hidden} x {width}, {tokens} tokens {dtype}")
+    want, bound = ref.moe(i["x"], i["experts"], i["weights"], i["gate"], i["up"], i["down"], group, bits)
+    check(run_moe(i), want, bound, f"{bits} bits g{group}")
+
+
 @pytest.mark.parametrize("tokens,experts,top_k", REGIMES)
 def test_moe_same_result_each_time_and_nothing_else_written(tokens, experts, top_k):
     i = moe_inputs(gen_of("again", tokens), tokens, experts, top_k, 160, 288, 5, 32, F16)
