@@ -15,9 +15,9 @@
 // would cost 1.5 times the rounding of y; these cost a hundredth. h has 11 bits and so loses no more.
 //
 // Measured (kernels alone): 2048 tokens through 8 of 128 x [768, 2048], 4 bits: sort 12.1 us, gate and up 165, down 129,
-// combine 24, 155 GFLOP in all; 512 tokens through 2 of 8 x [14336, 4096]: 434 and 340 us,
-// where the kernels for few rows take 3.8 ms. Bound by
-// what surrounds the products of a tile: 143 of 189 us stayed when all loads and dequantization were left out.
+// combine 24, 155 GFLOP in all; 512 tokens through 2 of 8 x [14336, 4096]: 434 and 340 us, where the kernels for few
+// rows take 3.8 ms. Bound by what surrounds the products of a tile: 143 of then 189 us stayed when all loads and
+// dequantization were left out.
 //
 // A workgroup of 4 waves has 128 rows of a weight, 32 a wave, dequantized once in registers by the wave that
 // multiplies them, against up to 5 x 32 rows of x from LDS (only as many as there are). Two workgroups share a
